@@ -291,13 +291,11 @@ def _plain_plan(st):
     dev, room = table.device, st["slot"].numel()
     goal = (kept + n + page - 1) // page
     bad = (kept < 0) | (n < 0) | (held < 0) | (held > max_pages) | (goal > max_pages) | (kept > held * page)
-    need = torch.where(bad, 0, (goal - held).clamp(min=0))
-    back = torch.where(bad, 0, (held - goal).clamp(min=0))
-    asked = torch.where(bad, 0, n)
-    top = count + back.sum()
-    ok = ~bad & (asked.cumsum(0) <= room) & ((need == 0) | (need.cumsum(0) <= top))
+    fits = ~bad & (torch.where(bad, 0, n).cumsum(0) <= room)
+    need = torch.where(fits, (goal - held).clamp(min=0), 0)
+    back = torch.where(fits, (held - goal).clamp(min=0), 0)
+    ok = fits & ((need == 0) | (need.cumsum(0) <= count + back.sum()))
     need, got = torch.where(ok, need, 0), torch.where(ok, n, 0)
-    back = torch.where(ok, back, 0)
     # returned pages go on top of the free list, in the order of the requests
     col = torch.arange(max_pages, device=dev)[None, :]
     freed = (col >= goal[:, None]) & (col < held[:, None]) & ok[:, None]
@@ -439,15 +437,16 @@ def _exact_plan(st):
     goal = [-(-(a + b) // page) for a, b in zip(kept, n)]
     bad = [a < 0 or b < 0 or h < 0 or h > W or t > W or a > h * page
            for a, b, h, t in zip(kept, n, held, goal)]
-    top = count + sum(max(h - t, 0) for h, t, x in zip(held, goal, bad) if not x)
-    asked, wanted, ok = 0, 0, []
+    asked, fits = 0, []
     for b in range(B):
-        if bad[b]:
-            ok.append(False)
-            continue
-        asked, need = asked + n[b], max(goal[b] - held[b], 0)
+        asked += 0 if bad[b] else n[b]
+        fits.append(not bad[b] and asked <= room)
+    top = count + sum(max(h - t, 0) for h, t, f in zip(held, goal, fits) if f)
+    wanted, ok = 0, []
+    for b in range(B):
+        need = max(goal[b] - held[b], 0) if fits[b] else 0
         wanted += need
-        ok.append(asked <= room and (need == 0 or wanted <= top))
+        ok.append(fits[b] and (need == 0 or wanted <= top))
     for b in range(B):
         if ok[b]:
             for t in range(goal[b], held[b]):
