@@ -309,6 +309,14 @@ namespace gva {
 // Lets other translation units of the library record a reason for gva_last_error.
 void set_error_message(const char* msg) { snprintf(g_err, sizeof(g_err), "%s", msg); }
 
+// The shape checks, TMA descriptor encoding and SM count, for the paged calls.
+gva_status_t shape_status(const gva_shape_t* shape) { return check_shape(shape, false); }
+gva_status_t encode_rows(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows,
+                         int box_cols, CUtensorMapSwizzle sw) {
+  return encode_2d(m, base, rows, cols, cols, box_rows, box_cols, sw);
+}
+int device_sms() { return num_sms(); }
+
 // gva_decode_attention that also zeroes the workspace's status word on the stream,
 // after validation and right before the split kernel (used by the entry point
 // whose scratch is shared by all calls).

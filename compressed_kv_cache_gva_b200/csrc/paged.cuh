@@ -1,0 +1,136 @@
+// Device helpers of the paged attention kernels: a sequence's query rows, the row
+// blocks a kernel cuts the batch into, and the walk of one CTA over its pieces.
+#pragma once
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace gva {
+
+// Query rows [r0, r0 + n) and cached length of sequence b; n = 0 where the sequence
+// is inconsistent or belongs to the other kernel of the call.
+struct SeqRows {
+  int r0, n, L;
+  bool bad;
+};
+
+__device__ __forceinline__ SeqRows seq_rows(const PagedArgs& a, int b) {
+  SeqRows s;
+  s.r0 = __ldg(a.q_start + b);
+  const int r1 = __ldg(a.q_start + b + 1);
+  s.L = __ldg(a.seq_len + b);
+  s.bad = s.r0 < 0 || r1 < s.r0 || r1 > a.n_rows || r1 - s.r0 > a.max_new || s.L < 0;
+  s.n = s.bad ? 0 : r1 - s.r0;
+  const int cols = s.n * a.hpr;   // n_rows * H fits 32 bits
+  if (cols <= a.lo_rows || cols > a.hi_rows) s.n = 0;
+  return s;
+}
+
+// One CTA reports what is inconsistent in the batch (whole block).
+__device__ inline void flag_bad_sequences(const PagedArgs& a) {
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+    const SeqRows s = seq_rows(a, b);
+    if (s.bad || (s.L > 0 && (long long)a.max_pages * a.page < s.L))
+      atomicOr(a.status, GVA_DEVERR_RANGE);
+  }
+}
+
+// Cache row of position t of sequence b; num_slots (a row outside the cache: TMA reads
+// zeros there) behind its end, or where the table is wrong (flagged).
+__device__ __forceinline__ int slot_of(const PagedArgs& a, const int* row, int t, int L) {
+  if (t >= L) return a.num_slots;
+  const int col = t / a.page;
+  int pg = -1;
+  if (col < a.max_pages) pg = __ldg(row + col);
+  if (pg < 0 || pg >= a.num_pages) {
+    atomicOr(a.status, GVA_DEVERR_RANGE);
+    return a.num_slots;
+  }
+  return pg * a.page + (t - col * a.page);
+}
+
+// ---------------------------------------------------------------------------
+// Row blocks.  The n * H/G query rows (token x head) of a value group of a sequence
+// are cut into blocks of M; block rb sees keys [0, kv_end) and takes
+// nt = max(1, ceil(kv_end / TK)) tiles (one masked tile where it sees none, which
+// yields its zeros).  A unit is one tile of one block; units are numbered by
+// sequence, block, group, tile, and CTA i takes units [i, i+1) * NT / grid: every CTA
+// gets the same number of tiles whatever the lengths, and a block whose units fall
+// to several CTAs is merged from their pieces.
+// ---------------------------------------------------------------------------
+template <int M, int TK>
+struct RowBlocks {
+  const PagedArgs& a;
+  __device__ __forceinline__ int blocks(const SeqRows& s) const { return (s.n * a.hpr + M - 1) / M; }
+  __device__ __forceinline__ int kv_end(const SeqRows& s, int rb) const {
+    const int last = min(s.n - 1, ((rb + 1) * M - 1) / a.hpr);
+    return max(0, s.L - s.n + last + 1);
+  }
+  __device__ __forceinline__ int tiles(const SeqRows& s, int rb) const {
+    return max(1, (kv_end(s, rb) + TK - 1) / TK);
+  }
+  __device__ long long units(int b) const {
+    const SeqRows s = seq_rows(a, b);
+    long long u = 0;
+    const int nb = blocks(s);
+    for (int rb = 0; rb < nb; ++rb) u += tiles(s, rb);
+    return u * a.G;
+  }
+};
+
+// A piece: tiles [k0, k1) of block rb of group g of sequence b, which has nt tiles.
+struct RowPiece {
+  int b, g, rb, k0, k1, nt;
+};
+
+// The pieces of a CTA's units [u, end), in order (one thread walks).
+template <int M, int TK>
+struct RowWalk {
+  RowBlocks<M, TK> rb;
+  const int* prefix;   // units before each sequence [B + 1], read by first() only
+  int u, end;
+  RowPiece p;
+  SeqRows s;
+  // first piece; false if the CTA has none
+  __device__ bool first() {
+    if (u >= end) return false;
+    p.b = seq_at(prefix, rb.a.B, u);
+    s = seq_rows(rb.a, p.b);
+    int rem = u - prefix[p.b];
+    p.rb = 0;
+    for (;;) {
+      p.nt = rb.tiles(s, p.rb);
+      if (rem < rb.a.G * p.nt) break;
+      rem -= rb.a.G * p.nt;
+      ++p.rb;
+    }
+    p.g = rem / p.nt;
+    p.k0 = rem - p.g * p.nt;
+    clip();
+    return true;
+  }
+  __device__ void clip() { p.k1 = min(p.nt, p.k0 + (end - u)); }
+  __device__ bool next() {
+    u += p.k1 - p.k0;
+    if (u >= end) return false;
+    p.k0 = 0;
+    if (++p.g == rb.a.G) {
+      p.g = 0;
+      if (++p.rb == rb.blocks(s)) {
+        p.rb = 0;
+        do s = seq_rows(rb.a, ++p.b); while (s.n == 0 && p.b + 1 < rb.a.B);
+      }
+      p.nt = rb.tiles(s, p.rb);
+    }
+    clip();
+    return true;
+  }
+};
+
+// Where a piece's partial state goes: a CTA leaves at most one block that it did not
+// start (slot 2 cta) and one that it started and does not end (slot 2 cta + 1).
+__device__ __forceinline__ int piece_slot(const RowPiece& p, int cta) {
+  return 2 * cta + (p.k0 == 0 ? 1 : 0);
+}
+
+}  // namespace gva

@@ -1,0 +1,524 @@
+// Paged attention of blocks of query rows on the fifth-generation tensor cores:
+// prompt chunks, and drafts too wide for the mma.sync kernel.
+//
+// A block is M = 128 query rows (new token x head of a value group) of one sequence:
+//   S[M x TK] = Q~_hi V^T + Q~_lo V^T + Qr_hi Kr^T + Qr_lo Kr^T   (tcgen05, TMEM)
+//   online softmax of the rows, fp32, base 2                       (4 warps)
+//   O[M x d_h] = alpha O + P V                                     (tcgen05, TMEM)
+// The fp32 query is split in bf16 hi + lo, so the scores keep ~16 bits.  P is bf16
+// where the output is (2^-9 relative, below the output's own rounding) and hi + lo
+// where the output is float32.
+//
+// Work: the tiles of all blocks, numbered in order, are cut evenly over a fixed grid
+// (paged.cuh).  A long chunk gives every CTA the same number of tiles although its
+// causal blocks differ in length; a few drafts on a long cache, which are one block
+// per group, are split over the keys as well.  A CTA walks its pieces; a block that
+// several CTAs share leaves partial states that the merge kernel joins.
+//
+// Roles: warp 0 streams tiles with 2-D TMA loads, one box per page (or part of one),
+// its lanes holding the cache rows of the next 32 boxes; one thread of warp 1 issues
+// every MMA; warps 4..7 (a TMEM lane quarter each) do the softmax, write P to shared
+// memory and rescale O only when a row's maximum grew by more than 2^8.  All ring and
+// buffer barriers count tiles over the whole CTA, so they run on across pieces.
+#include "launch.h"
+#include "paged.cuh"
+#include "tc.cuh"
+
+namespace gva {
+
+namespace {
+
+template <int D_H_, int DRP_, bool HILO_>
+struct PtCfg {
+  static constexpr int D_H = D_H_, DRP = DRP_;
+  static constexpr bool HILO = HILO_;        // P in two bf16 halves (float32 output)
+  static constexpr int M = kPagedTcRows;
+  // keys per tile: 128 with d_h = 128 (one CTA per SM either way, half the score
+  // instructions), 64 with d_h = 64 (two CTAs per SM hide each other's hand-offs)
+  static constexpr int TK = D_H == 128 && !HILO ? 128 : 64;
+  static constexpr int CB = D_H / 64, KS = D_H / 16, RS = DRP / 16;
+  static constexpr int STAGES = (TK == 128 && D_H == 128) ? 2 : 3;
+  static constexpr int QB = M * D_H * 2;     // q~ hi (or lo): CB blocks of M rows x 128 B
+  static constexpr int QRB = DRP ? (M * DRP * 2 + 1023) / 1024 * 1024 : 0;
+  static constexpr int PH = M * TK * 2;      // one half of P: TK/64 blocks of M rows x 128 B
+  static constexpr int PB = HILO ? 2 * PH : PH;
+  static constexpr int VB = CB * TK * 128;
+  static constexpr int KRB = DRP * TK * 2;
+  static constexpr int STAGE = VB + (KRB + 1023) / 1024 * 1024;
+  static constexpr int OFF_QR = 2 * QB, OFF_P = OFF_QR + 2 * QRB, OFF_RING = OFF_P + 2 * PB;
+  static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
+  // full[S], empty[S], s_full[2], s_free[2], p_full[2], pv_done[2], fin
+  static constexpr int NBAR = 2 * STAGES + 9;
+  // the unit prefix of the prologue lies where P goes later
+  static constexpr int SMEM = 1024 + OFF_BAR + NBAR * 8 + 8;
+  static constexpr uint32_t S_COL = 0, O_COL = 2 * TK;
+  static constexpr uint32_t TMEM_COLS = O_COL + D_H > 256 ? 512 : 256;
+  static constexpr uint32_t TX = VB + KRB;
+  static constexpr int THREADS = 256;
+  static constexpr uint32_t SW_R = DRP == 32 ? tc::kSw64 : tc::kSw32;
+  static constexpr uint32_t SBO_R = DRP * 2 * 8;
+  // CTAs per SM that shared and tensor memory hold: registers are budgeted for them
+  static constexpr int PER_SM = 2 * (SMEM + 1024) <= 227 * 1024 && 2 * TMEM_COLS <= 512 ? 2 : 1;
+  static_assert(2 * PB >= (int)sizeof(int) * (kMaxBatch + 1) + 16 + 33 * 8, "unit prefix");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// 16-byte chunk of a row in a swizzled K-major tile (rows of 128, 64 or 32 bytes).
+__device__ __forceinline__ uint32_t sw128(int r, int chunk) {
+  return (uint32_t)(r * 128 + ((chunk ^ (r & 7)) << 4));
+}
+template <int DRP>
+__device__ __forceinline__ uint32_t sw_pos(int r, int chunk) {
+  return DRP == 32 ? (uint32_t)(r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4))
+                   : (uint32_t)(r * 32 + ((chunk ^ ((r >> 2) & 1)) << 4));
+}
+
+__device__ __forceinline__ uint4 split_bf16(const float* x, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = x[2 * i], b = x[2 * i + 1], ah = bf16_round(a), bh = bf16_round(b);
+    h[i] = pack_bf16(ah, bh);
+    l[i] = pack_bf16(a - ah, b - bh);
+  }
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::PER_SM)
+    paged_tc_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_kr) {
+  extern __shared__ unsigned char smraw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(sm);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
+  const uint32_t full = smem_u32(bars), empty = full + 8 * C::STAGES;
+  const uint32_t s_full = empty + 8 * C::STAGES, s_free = s_full + 16;
+  const uint32_t p_full = s_free + 16, pv_done = p_full + 16, fin = pv_done + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
+  int* prefix = reinterpret_cast<int*>(sm + C::OFF_P);
+  long long* wtmp = reinterpret_cast<long long*>(
+      (reinterpret_cast<uintptr_t>(prefix + a.B + 1) + 15) & ~uintptr_t(15));
+  __shared__ RowPiece piece;
+  __shared__ int more;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hpr = a.hpr;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(s_free + 8 * i, 4);
+      mbar_init(p_full + 8 * i, 4);
+      mbar_init(pv_done + 8 * i, 1);
+    }
+    mbar_init(fin, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tc::relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_v);
+    if (C::DRP) prefetch_tmap(&tm_kr);
+  }
+  // queries, lengths, tables and cache rows may come from the kernels before
+  pdl_wait();
+  pdl_trigger();   // the merge waits for this kernel before it reads
+  if (blockIdx.x == 0 && a.flag_errors) flag_bad_sequences(a);
+  const RowBlocks<C::M, C::TK> blocks{a};
+  if (block_scan(a.B, [&](int b) { return blocks.units(b); }, prefix, wtmp) >= (1ll << 31) &&
+      threadIdx.x == 0)
+    atomicOr(a.status, GVA_DEVERR_RANGE);
+  const TileSplit ts = make_split(prefix[a.B], (int)gridDim.x, 0);
+  RowWalk<C::M, C::TK> walk{blocks, prefix, ts.first(blockIdx.x), ts.first(blockIdx.x + 1), {}, {}};
+  if (threadIdx.x == 0) {
+    a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    more = walk.first();
+    piece = walk.p;
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // kt: tiles of this CTA before the piece; all barrier phases count from it
+  int kt = 0, issued = 0;
+  bool ok = true;   // false once a bounded wait gave up: skip work, keep the order
+  while (more) {
+    const RowPiece p = piece;
+    const SeqRows s = seq_rows(a, p.b);
+    const int row0 = p.rb * C::M, rows = min(C::M, s.n * hpr - row0);
+    const int nk = p.k1 - p.k0;
+
+    // ---- queries -> shared memory: bf16 hi and lo halves, swizzled K-major rows
+    const int dq = C::D_H + a.d_r;
+    for (int e = threadIdx.x; e < C::M * (C::D_H / 8); e += C::THREADS) {
+      const int r = e / (C::D_H / 8), c = e % (C::D_H / 8);
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (r < rows) {
+        const int R = row0 + r;
+        const float* src = a.q_abs + ((long long)(s.r0 + R / hpr) * a.H + p.g * hpr + R % hpr) * dq + c * 8;
+        const float4 u = *reinterpret_cast<const float4*>(src);
+        const float4 v = *reinterpret_cast<const float4*>(src + 4);
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+      }
+      uint4 lo;
+      const uint4 hi = split_bf16(x, lo);
+      const uint32_t o = (c / 8) * (C::M * 128) + sw128(r, c % 8);
+      *reinterpret_cast<uint4*>(sm + o) = hi;
+      *reinterpret_cast<uint4*>(sm + o + C::QB) = lo;
+    }
+    if constexpr (C::DRP > 0) {
+      for (int e = threadIdx.x; e < C::M * (C::DRP / 8); e += C::THREADS) {
+        const int r = e / (C::DRP / 8), c = e % (C::DRP / 8), R = row0 + r;
+        const float* src = a.q_abs + ((long long)(s.r0 + R / hpr) * a.H + p.g * hpr + R % hpr) * dq + C::D_H;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (r < rows && c * 8 + i < a.d_r) ? src[c * 8 + i] : 0.f;
+        uint4 lo;
+        const uint4 hi = split_bf16(x, lo);
+        const uint32_t o = C::OFF_QR + sw_pos<C::DRP>(r, c);
+        *reinterpret_cast<uint4*>(sm + o) = hi;
+        *reinterpret_cast<uint4*>(sm + o + C::QRB) = lo;
+      }
+    }
+    fence_proxy_async_smem();   // the queries are read by the tensor core (async proxy)
+    __syncthreads();
+
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      const int per_tile = C::TK >> a.box_log2;
+      const int* row = a.table + (long long)p.b * a.table_stride;
+      int base = p.k0 * per_tile;
+      const int end = p.k1 * per_tile;
+      auto look = [&](int i) { return i < end ? slot_of(a, row, i << a.box_log2, s.L) : a.num_slots; };
+      int y_now = look(base + lane), y_next = look(base + 32 + lane);
+      for (int k = 0; k < nk; ++k) {
+        const int box0 = (p.k0 + k) * per_tile;
+        if (box0 - base >= 32) {
+          base += 32;
+          y_now = y_next;
+          y_next = look(base + 32 + lane);
+        }
+        const int kk = kt + k, sg = kk % C::STAGES;
+        if (ok && kk >= C::STAGES) ok = mbar_wait(empty + 8 * sg, ((kk / C::STAGES) - 1) & 1, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t fb = full + 8 * sg, st = sb + C::OFF_RING + sg * C::STAGE;
+        if (lane == 0) mbar_arrive_expect_tx(fb, C::TX);
+        __syncwarp();
+        for (int j = 0; j < per_tile; ++j) {
+          const int y = __shfl_sync(0xffffffffu, y_now, box0 + j - base);
+          if (lane == 0) {
+            const uint32_t r = (uint32_t)j << a.box_log2;
+#pragma unroll
+            for (int c = 0; c < C::CB; ++c)
+              tma_load_2d(st + c * C::TK * 128 + r * 128, &tm_v, p.g * C::D_H + c * 64, y, fb);
+            if constexpr (C::DRP > 0) tma_load_2d(st + C::VB + r * C::DRP * 2, &tm_kr, 0, y, fb);
+          }
+        }
+        issued = kk + 1;
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issue
+      if (lane == 0) {
+        constexpr uint32_t idS = tc::idesc_bf16(C::M, C::TK, 0, 0);   // Q (K-major) x V^T (K-major)
+        constexpr uint32_t idO = tc::idesc_bf16(C::M, C::D_H, 0, 1);  // P (K-major) x V (MN-major)
+        for (int k = 0; k <= nk; ++k) {
+          if (k < nk) {
+            const int kk = kt + k, sg = kk % C::STAGES;
+            ok = ok && mbar_wait(full + 8 * sg, (kk / C::STAGES) & 1, a.status);
+            if (kk >= 2) ok = ok && mbar_wait(s_free + 8 * (kk & 1), ((kk - 2) >> 1) & 1, a.status);
+            tc::fence_after();
+            if (ok) {
+              const uint32_t d = tmem + C::S_COL + (kk & 1) * C::TK;
+              const uint32_t vt = sb + C::OFF_RING + sg * C::STAGE;
+#pragma unroll
+              for (int ks = 0; ks < C::KS; ++ks) {
+                const uint32_t kb = (ks >> 2) * (C::M * 128) + (ks & 3) * 32;
+                const uint64_t bq =
+                    tc::smem_desc(vt + (ks >> 2) * (C::TK * 128) + (ks & 3) * 32, 16, 1024, tc::kSw128);
+                tc::mma_bf16(d, tc::smem_desc(sb + kb, 16, 1024, tc::kSw128), bq, idS, ks > 0);
+                tc::mma_bf16(d, tc::smem_desc(sb + C::QB + kb, 16, 1024, tc::kSw128), bq, idS, 1);
+              }
+#pragma unroll
+              for (int rs = 0; rs < C::RS; ++rs) {
+                const uint64_t bk = tc::smem_desc(vt + C::VB + rs * 32, 16, C::SBO_R, C::SW_R);
+                tc::mma_bf16(d, tc::smem_desc(sb + C::OFF_QR + rs * 32, 16, C::SBO_R, C::SW_R), bk, idS, 1);
+                tc::mma_bf16(d, tc::smem_desc(sb + C::OFF_QR + C::QRB + rs * 32, 16, C::SBO_R, C::SW_R), bk,
+                             idS, 1);
+              }
+            }
+            tc::commit(s_full + 8 * (kk & 1));
+          }
+          if (k >= 1) {   // P.V of the tile before
+            const int kp = kt + k - 1, sp = kp % C::STAGES, pb = kp & 1;
+            ok = ok && mbar_wait(p_full + 8 * pb, (kp >> 1) & 1, a.status);
+            tc::fence_after();
+            if (ok) {
+              const uint32_t vt = sb + C::OFF_RING + sp * C::STAGE;
+#pragma unroll
+              for (int h = 0; h < (C::HILO ? 2 : 1); ++h) {
+                const uint32_t pt = sb + C::OFF_P + pb * C::PB + h * C::PH;
+#pragma unroll
+                for (int kk = 0; kk < C::TK / 16; ++kk)
+                  tc::mma_bf16(tmem + C::O_COL,
+                               tc::smem_desc(pt + (kk >> 2) * (C::M * 128) + (kk & 3) * 32, 16, 1024,
+                                             tc::kSw128),
+                               tc::smem_desc(vt + kk * 16 * 128, C::TK * 128, 1024, tc::kSw128), idO,
+                               (k > 1 || h > 0 || kk > 0) ? 1u : 0u);
+              }
+            }
+            tc::commit(pv_done + 8 * pb);
+            tc::commit(empty + 8 * sp);
+          }
+        }
+      }
+    } else if (warp >= 4) {
+      // ---------------------------------------------------------- softmax, P, O rescale, output
+      const int quarter = warp & 3, r = 32 * quarter + lane;
+      const bool valid = r < rows, idle = 32 * quarter >= rows;   // idle: no row of this warp counts
+      const int R = row0 + r, qi = R / hpr, head = p.g * hpr + R % hpr;
+      const int lim = s.L - s.n + qi;                             // last key of this row
+      const int kv_all = s.L - s.n + row0 / hpr + 1;              // keys every row sees
+      const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < nk; ++k) {
+        const int kk = kt + k, pb = kk & 1, t0 = (p.k0 + k) * C::TK;
+        ok = ok && mbar_wait(s_full + 8 * pb, (kk >> 1) & 1, a.status);
+        tc::fence_after();
+        float x[C::TK];
+        float alpha = 1.f;
+        uint8_t* prow = sm + C::OFF_P + pb * C::PB;
+        if (idle) {
+          // rows past the block: their P only has to be finite (their O is never read)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free + 8 * pb);
+          if (kk >= 2) {
+            ok = ok && mbar_wait(pv_done + 8 * pb, ((kk - 2) >> 1) & 1, a.status);
+            tc::fence_after();
+          }
+          if (k < 2) {
+#pragma unroll
+            for (int c = 0; c < C::PB / (C::M * 16); ++c)
+              *reinterpret_cast<uint4*>(prow + (c >> 3) * (C::M * 128) + sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
+          }
+        } else {
+#pragma unroll
+          for (int q4 = 0; q4 < C::TK / 16; ++q4) tc::ld16(trow + C::S_COL + pb * C::TK + q4 * 16, x + q4 * 16);
+          tc::wait_ld();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free + 8 * pb);
+          float mx = -INFINITY;
+          if (ok && t0 + C::TK <= kv_all) {   // every row sees the whole tile: no mask
+#pragma unroll
+            for (int j = 0; j < C::TK; ++j) mx = fmaxf(mx, x[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < C::TK; ++j) {
+              const bool vis = ok && valid && t0 + j <= lim && t0 + j < s.L;
+              x[j] = vis ? x[j] : -INFINITY;
+              mx = fmaxf(mx, x[j]);
+            }
+          }
+          // a row keeps the maximum its exponentials are taken against until a tile
+          // exceeds it by more than 8 (log2 units): P <= 2^8, and O is touched only then
+          const bool grow = mx > m + 8.f;
+          const float mn = grow ? mx : m;
+          const float ms = mn == -INFINITY ? 0.f : mn;
+          alpha = ex2(m - ms);
+          if (kk >= 2) {   // P buffer free: the P.V of two tiles ago has completed
+            ok = ok && mbar_wait(pv_done + 8 * pb, ((kk - 2) >> 1) & 1, a.status);
+            tc::fence_after();
+          }
+          float rsum = 0.f;
+#pragma unroll
+          for (int c = 0; c < C::TK / 8; ++c) {
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              e[i] = ex2(x[8 * c + i] - ms);
+              rsum += e[i];
+            }
+            const uint32_t o = (c >> 3) * (C::M * 128) + sw128(r, c & 7);
+            if constexpr (C::HILO) {
+              uint4 lo;
+              *reinterpret_cast<uint4*>(prow + o) = split_bf16(e, lo);
+              *reinterpret_cast<uint4*>(prow + C::PH + o) = lo;
+            } else {
+              *reinterpret_cast<uint4*>(prow + o) = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
+                                                               pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
+            }
+          }
+          l = l * alpha + rsum;
+          m = mn;
+        }
+        // value rows behind the sequence meet P = 0 but may hold anything (NaN): zero
+        // them before the P.V product reads them
+        if (t0 + C::TK > s.L) {
+          uint8_t* vt = sm + C::OFF_RING + (kk % C::STAGES) * C::STAGE;
+          const int r_lo = max(s.L - t0, 0), nz = (C::TK - r_lo) * 8;   // 16-byte chunks per block
+          for (int e = r; e < nz * C::CB; e += 128) {
+            const int c = e / nz, i = e % nz;
+            *reinterpret_cast<uint4*>(vt + c * C::TK * 128 + (r_lo + i / 8) * 128 + (i % 8) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+        }
+        // O *= alpha before this tile's P.V, once the previous one has completed
+        if (k >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          ok = ok && mbar_wait(pv_done + 8 * ((kk - 1) & 1), ((kk - 1) >> 1) & 1, a.status);
+          tc::fence_after();
+#pragma unroll
+          for (int q4 = 0; q4 < C::D_H / 16; ++q4) {
+            float o[16];
+            tc::ld16(trow + C::O_COL + q4 * 16, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tc::st16(trow + C::O_COL + q4 * 16, o);
+          }
+          tc::wait_st();
+        }
+        fence_proxy_async_smem();   // P and the zeroed rows are read by the tensor core
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * pb);
+      }
+      {   // the last P.V of the piece (and with it every MMA before) has completed
+        const int kl = kt + nk - 1;
+        ok = ok && mbar_wait(pv_done + 8 * (kl & 1), (kl >> 1) & 1, a.status);
+        tc::fence_after();
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!idle) {
+        const bool whole = nk == p.nt;
+        const long long orow = (long long)(s.r0 + qi) * a.H + head;
+        const long long prt = (long long)piece_slot(p, blockIdx.x) * C::M + r;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int q4 = 0; q4 < C::D_H / 16; ++q4) {
+          float o[16];
+          tc::ld16(trow + C::O_COL + q4 * 16, o);
+          tc::wait_ld();
+          if (valid && ok) {
+            if (!whole) {
+              float4* dst = reinterpret_cast<float4*>(a.part_o + prt * C::D_H + q4 * 16);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            } else if (a.out_bf16) {
+              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * C::D_H + q4 * 16);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                    pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                    pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                    pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * C::D_H + q4 * 16);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+            }
+          }
+        }
+        if (valid && ok) {
+          if (!whole) a.part_ml[prt] = make_float2(m, l);
+          else if (a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+      }
+      tc::fence_before();   // O has been read: the next piece's MMAs may overwrite it
+    }
+    kt += nk;
+    if (threadIdx.x == 0) {
+      if (p.k0 == 0 && nk < p.nt)   // started here, ended elsewhere: where its pieces are
+        a.meta[blockIdx.x] = make_int4(ts.cta_of(walk.u + p.nt - 1) - (int)blockIdx.x + 1, p.b, p.g, p.rb);
+      more = walk.next();
+      piece = walk.p;
+    }
+    __syncthreads();   // all roles are done with the piece; the next one's is in place
+    tc::fence_after();
+  }
+
+  // ---- nothing in flight may outlive the CTA: copies, then MMAs; free the memory
+  if (warp == 0 && lane == 0) {
+    for (int kk = max(0, issued - C::STAGES); kk < issued; ++kk)
+      mbar_wait(full + 8 * (kk % C::STAGES), (kk / C::STAGES) & 1, a.status);
+  }
+  if (warp == 1 && lane == 0) {
+    tc::commit(fin);
+    mbar_wait(fin, 0, a.status);
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after();
+    tc::dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Visit the configuration of (d_h, padded d_r, output type).
+template <class F>
+bool dispatch(const gva_shape_t& sh, F&& f) {
+  const int drp = sh.d_r == 0 ? 0 : (sh.d_r <= 16 ? 16 : (sh.d_r <= 32 ? 32 : -1));
+  const bool hilo = sh.out_dtype == GVA_F32;
+#define GVA_PT(DH, DRP, HILO)                                   \
+  if (sh.d_h == DH && drp == DRP && hilo == HILO) {             \
+    f(PtCfg<DH, DRP, HILO>{});                                  \
+    return true;                                                \
+  }
+#define GVA_PT_DR(DH, HILO) GVA_PT(DH, 0, HILO) GVA_PT(DH, 16, HILO) GVA_PT(DH, 32, HILO)
+  GVA_PT_DR(64, false)
+  GVA_PT_DR(64, true)
+  GVA_PT_DR(128, false)
+  GVA_PT_DR(128, true)
+#undef GVA_PT_DR
+#undef GVA_PT
+  return false;
+}
+
+}  // namespace
+
+bool paged_tc_supported(const gva_shape_t& sh, int page) {
+  return sh.cache_dtype == GVA_BF16 && page % 8 == 0 && dispatch(sh, [](auto) {});
+}
+
+int paged_tc_tile(const gva_shape_t& sh) {
+  int tk = 0;
+  dispatch(sh, [&](auto c) { tk = decltype(c)::TK; });
+  return tk;
+}
+
+int paged_tc_grid(const gva_shape_t& sh, int n_rows, int num_sms, long long max_total) {
+  int tk = 64, per_sm = 1;
+  dispatch(sh, [&](auto c) {
+    tk = decltype(c)::TK;
+    per_sm = decltype(c)::PER_SM;
+  });
+  // no more CTAs than blocks x tiles could be
+  const long long blocks = ((long long)n_rows * (sh.H / sh.G) + kPagedTcRows - 1) / kPagedTcRows + sh.B;
+  const long long want = blocks * sh.G * (max_total / tk + 1);
+  const long long grid = (long long)num_sms * per_sm;
+  return (int)(want < grid ? want : grid);
+}
+
+cudaError_t launch_paged_tc(const gva_shape_t& sh, const PagedArgs& a, const CUtensorMap& tv,
+                            const CUtensorMap& tk, cudaStream_t st) {
+  cudaError_t err = cudaErrorNotSupported;
+  dispatch(sh, [&](auto c) {
+    using C = decltype(c);
+    const size_t smem = C::SMEM;
+    if ((err = ensure_max_smem(paged_tc_kernel<C>, smem)) != cudaSuccess) return;
+    err = launch_pdl(paged_tc_kernel<C>, dim3(a.grid), dim3(C::THREADS), smem, st, a, tv, tk);
+  });
+  return err;
+}
+
+}  // namespace gva

@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libgva.so")
 F32, BF16 = 0, 1
 FLAG_FMA_PATH = 1
 FLAG_TCGEN05_PATH = 2
-DEVERR_RANGE, DEVERR_WAIT = 1, 2
+DEVERR_RANGE, DEVERR_WAIT, DEVERR_PAGES = 1, 2, 4
 
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "workspace too small",
            4: "CUDA error"}
@@ -111,6 +111,15 @@ def load(path: str) -> ctypes.CDLL:
     L.gva_decode_attention_noalloc.argtypes = [SP, P, P, P, P, P, I64, I64, P, P, P]
     L.gva_noalloc_status.restype = ctypes.c_int
     L.gva_noalloc_status.argtypes = [P, P]
+    L.gva_plan_pages.restype = ctypes.c_int
+    L.gva_plan_pages.argtypes = [I32, I32, I32, I32, I64, I32] + [P] * 15
+    L.gva_paged_workspace_size.restype = SZ
+    L.gva_paged_workspace_size.argtypes = [SP, I32, I32, I32, I64]
+    L.gva_paged_attention.restype = ctypes.c_int
+    L.gva_paged_attention.argtypes = [SP, I32, P, P, P, I64, P, I32, I64, P, P, I32, I32, I64, P, P, P,
+                                      SZ, P]
+    L.gva_verify_draft.restype = ctypes.c_int
+    L.gva_verify_draft.argtypes = [I32, I32, I32, P, P, I32, P, I64, P, I64, P, P, P, P, P, P, P, P]
     return L
 
 
@@ -264,9 +273,127 @@ def noalloc_status(stream=None) -> int:
     return int(buf.item())
 
 
+def _arr(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    """Pointer of a contiguous tensor of this type and shape on the current device."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must live on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, rows: int, cols: int, dev: int):
+    """Pointer of a [rows, >= cols] matrix whose rows may be strided but are dense."""
+    if t.dtype not in dtypes or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols:
+        raise ValueError(f"{name}: expected {dtypes[0]} [{rows}, >= {cols}], got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must live on the current CUDA device")
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows must be dense and must not overlap")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def plan_pages(page_size: int, num_pages: int, kept_len, n_new, held_in, held_out, free_pages,
+               free_count_in, free_count_out, block_table, q_start, seq_len, n_granted, slot, pos,
+               err_flag=None, stream=None):
+    """gva_plan_pages: block tables, slots and positions of one step's new tokens.
+
+    int32 tensors: kept_len, n_new, held_in, held_out, seq_len, n_granted [B]; free_pages
+    [num_pages]; free_count_in, free_count_out, err_flag [1]; block_table [B, max_pages]
+    (rows may be strided); q_start [B + 1]; slot, pos [max_new_tokens].  held_out may be
+    held_in, and free_count_out free_count_in."""
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    B, m = kept_len.shape[0], slot.shape[0]
+    table = _rows(block_table, "block_table", (i32,), B, 1, dev)
+    _check(lib().gva_plan_pages(
+        B, int(page_size), int(num_pages), block_table.shape[1], _row_stride(block_table), m,
+        _arr(kept_len, "kept_len", i32, (B,), dev), _arr(n_new, "n_new", i32, (B,), dev),
+        _arr(held_in, "held_in", i32, (B,), dev), _arr(held_out, "held_out", i32, (B,), dev),
+        _arr(free_pages, "free_pages", i32, (num_pages,), dev),
+        _arr(free_count_in, "free_count_in", i32, (1,), dev),
+        _arr(free_count_out, "free_count_out", i32, (1,), dev), table,
+        _arr(q_start, "q_start", i32, (B + 1,), dev), _arr(seq_len, "seq_len", i32, (B,), dev),
+        _arr(n_granted, "n_granted", i32, (B,), dev), _arr(slot, "slot", i32, (m,), dev),
+        _arr(pos, "pos", i32, (m,), dev),
+        None if err_flag is None else _arr(err_flag, "err_flag", i32, (1,), dev), _stream(stream)))
+
+
+def paged_workspace_size(shape: Shape, page_size: int, n_rows: int, max_query_len: int,
+                         max_total_tokens: int) -> int:
+    return int(lib().gva_paged_workspace_size(ctypes.byref(shape), int(page_size), int(n_rows),
+                                              int(max_query_len), int(max_total_tokens)))
+
+
+def new_paged_workspace(shape: Shape, page_size: int, n_rows: int, max_query_len: int,
+                        max_total_tokens: int, device=None) -> torch.Tensor:
+    """A zeroed workspace for paged_attention (the status word must start at 0)."""
+    n = paged_workspace_size(shape, page_size, n_rows, max_query_len, max_total_tokens)
+    if n == 0:
+        raise GVAError(1, lib().gva_last_error().decode())
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+_TORCH = {F32: torch.float32, BF16: torch.bfloat16}
+
+
+def paged_attention(shape: Shape, page_size: int, q_abs, V_cache, kr_cache, block_table, q_start,
+                    seq_len, max_query_len: int, max_total_tokens: int, out, lse=None,
+                    workspace=None, stream=None):
+    """gva_paged_attention: the last n_b tokens of every request over its pages.
+
+    q_abs [n_rows, H, d_h + d_r] float32; V_cache [num_slots, G, d_h] and kr_cache
+    [num_slots, d_r] (None if d_r == 0); block_table [B, max_pages] int32 (rows may be
+    strided); q_start [B + 1] and seq_len [B] int32; out [n_rows, H, d_h]; lse [n_rows, H]."""
+    dev, i32, f32 = torch.cuda.current_device(), torch.int32, torch.float32
+    B, H, G, d_h, d_r = shape.B, shape.H, shape.G, shape.d_h, shape.d_r
+    n, slots, cache = q_abs.shape[0], V_cache.shape[0], _TORCH.get(shape.cache_dtype)
+    if workspace is None or not workspace.is_cuda or workspace.get_device() != dev:
+        raise ValueError("workspace must live on the current CUDA device")
+    _check(lib().gva_paged_attention(
+        ctypes.byref(shape), int(page_size), _arr(q_abs, "q_abs", f32, (n, H, d_h + d_r), dev),
+        _arr(V_cache, "V_cache", cache, (slots, G, d_h), dev),
+        None if d_r == 0 else _arr(kr_cache, "kr_cache", cache, (slots, d_r), dev), slots,
+        _rows(block_table, "block_table", (i32,), B, 1, dev), block_table.shape[1],
+        _row_stride(block_table), _arr(q_start, "q_start", i32, (B + 1,), dev),
+        _arr(seq_len, "seq_len", i32, (B,), dev), n, int(max_query_len), int(max_total_tokens),
+        _arr(out, "out", _TORCH.get(shape.out_dtype), (n, H, d_h), dev),
+        None if lse is None else _arr(lse, "lse", f32, (n, H), dev), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def verify_draft(vocab: int, tokens, q_start, target_probs, draft_probs, u_accept, u_sample,
+                 out_tokens, n_accepted, seq_len=None, kept_len=None, err_flag=None, stream=None):
+    """gva_verify_draft: which drafted tokens stay, and the token that follows them.
+
+    tokens, out_tokens [n_rows] int32; q_start [B + 1] int32; target_probs and draft_probs
+    [n_rows, >= vocab] float32 or bfloat16 (rows may be strided; draft_probs None: the
+    drafts were not drawn); u_accept [n_rows], u_sample [B] float32; n_accepted, seq_len,
+    kept_len [B] int32."""
+    dev, i32, f32 = torch.cuda.current_device(), torch.int32, torch.float32
+    n, B, dt = tokens.shape[0], u_sample.shape[0], target_probs.dtype
+    opt = lambda t, name, k: None if t is None else _arr(t, name, i32, (k,), dev)
+    target = _rows(target_probs, "target_probs", (f32, torch.bfloat16), n, vocab, dev)
+    draft = None if draft_probs is None else _rows(draft_probs, "draft_probs", (dt,), n, vocab, dev)
+    _check(lib().gva_verify_draft(
+        B, int(vocab), n, _arr(tokens, "tokens", i32, (n,), dev),
+        _arr(q_start, "q_start", i32, (B + 1,), dev), dtype_code(dt), target,
+        _row_stride(target_probs), draft, 0 if draft is None else _row_stride(draft_probs),
+        _arr(u_accept, "u_accept", f32, (n,), dev), _arr(u_sample, "u_sample", f32, (B,), dev),
+        _arr(out_tokens, "out_tokens", i32, (n,), dev), _arr(n_accepted, "n_accepted", i32, (B,), dev),
+        opt(seq_len, "seq_len", B), opt(kept_len, "kept_len", B), opt(err_flag, "err_flag", 1),
+        _stream(stream)))
+
+
 EXPORTS = ["gva_status_string", "gva_last_error", "gva_absorb_query", "gva_append_cache",
            "gva_decode_workspace_size", "gva_decode_attention", "gqa_decode_attention",
            "gva_decode_step", "gva_merge_states", "gva_decode_workspace_size_multi",
            "gva_decode_attention_multi", "gva_decode_attention_noalloc",
            "gva_shared_kv_decode_attention", "gqa_append_cache", "gqa_decode_step",
-           "gva_noalloc_status"]
+           "gva_noalloc_status", "gva_plan_pages", "gva_paged_workspace_size", "gva_paged_attention",
+           "gva_verify_draft"]

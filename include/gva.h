@@ -162,6 +162,7 @@ size_t gva_decode_workspace_size(const gva_shape_t* shape, int64_t max_total_tok
 
 #define GVA_DEVERR_RANGE 1   /* some sequence's slots leave [0, num_slots); those rows read as 0 */
 #define GVA_DEVERR_WAIT 2    /* a pipeline wait hit its poll or time limit; outputs invalid */
+#define GVA_DEVERR_PAGES 4   /* gva_plan_pages: some request got no pages or token room */
 
 /*
  * gva_decode_attention — one GVA decode step over a (possibly ragged) batch,
@@ -404,6 +405,173 @@ gva_status_t gva_decode_attention_noalloc(const gva_shape_t* shape, const float*
  * (the scratch's address or the copy failed).
  */
 gva_status_t gva_noalloc_status(int32_t* status_out, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Serving over a paged cache.
+ *
+ * The cache is an array of pages of page_size token slots, in the layout of the
+ * other calls: slot = page * page_size + offset, V_cache [num_pages * page_size, G,
+ * d_h], kr_cache [num_pages * page_size, d_r].  Row b of the block table names the
+ * pages of request b in order, so its token at position p lies in slot
+ * table[b][p / page_size] * page_size + p % page_size.  The pages have no counterpart
+ * in the paper, which caches one contiguous sequence (onedev.kr review, "What
+ * differs"); they change where a row lies and nothing of the method.
+ *
+ * One step of a server: gva_plan_pages (lengths -> pages, slots, positions),
+ * gva_append_cache (new tokens, by slot), gva_absorb_query (queries, by position),
+ * gva_paged_attention, and, for drafted tokens, gva_verify_draft, whose kept_len is
+ * the next plan's input.  None of the three calls below reads an input before the
+ * work before it on the stream has completed, so any kernel may produce them.
+ * ---------------------------------------------------------------------------- */
+
+/*
+ * gva_plan_pages — block tables, slots and positions of one step's new tokens, from
+ * the requests' lengths, on the GPU.
+ *
+ * Request b keeps kept_len[b] cached tokens and brings n_new[b] >= 0 new ones; after
+ * the call it holds goal = ceil((kept_len + n_new) / page_size) pages.  Pages above
+ * that (rejected drafts; a finished request passes 0 and 0) are returned, requests
+ * that need more get them, all in request order:
+ *   1. tokens: a request fits while the sum of n_new up to and including it is at
+ *      most max_new_tokens;
+ *   2. returned pages of the requests that fit go on top of the free list, in order
+ *      of request and table column;
+ *   3. a request that needs no page is granted; one that needs some is granted while
+ *      the pages needed up to and including it are at most those on the list, and
+ *      takes them from the top.
+ * A request that is not granted keeps its kept tokens and all its pages, brings none
+ * (n_granted = 0), and GVA_DEVERR_PAGES is set.  Inconsistent requests (a negative
+ * length, more kept tokens than its pages hold, a goal above max_pages) are treated
+ * the same, with seq_len = 0, and set GVA_DEVERR_RANGE, as does a free list whose
+ * count cannot be right (then nothing moves) and a page id outside [0, num_pages)
+ * met on the way to a slot (slot -1).
+ *
+ *   B             requests, [0, 4096];  page_size >= 1, num_pages >= 1, max_pages >= 1
+ *                 (num_pages * page_size and max_pages * page_size below 2^31)
+ *   kept_len, n_new, held_in     device [B] int32; held_in: pages each request holds
+ *   held_out      device [B] int32, may be held_in
+ *   free_pages    device [num_pages] int32, updated in place: a stack of free page ids
+ *   free_count_in, free_count_out   device [1] int32, may be the same
+ *   block_table   device [B, max_pages] int32, rows table_stride elements apart,
+ *                 updated in place: new pages are written, other entries left as they were
+ *   q_start       device [B + 1] int32: prefix sums of the granted tokens
+ *   seq_len       device [B] int32: kept plus granted tokens;  n_granted device [B] int32
+ *   slot, pos     device [max_new_tokens] int32: slot and position of new token i of
+ *                 request b at q_start[b] + i; entries past q_start[B] are set to -1
+ *                 (gva_append_cache skips such a token, and sets its err_flag)
+ *   err_flag      device int32 or NULL: GVA_DEVERR_* bits are or-ed in, never cleared
+ * One launch.  Inputs and outputs other than the pairs named above must not overlap.
+ * The entries of held_in and free_count_in are all read before any output is written.
+ * Errors: GVA_ERR_INVALID_ARG.  B == 0 sets q_start[0] = 0, the slots to -1 and the
+ * count.
+ */
+gva_status_t gva_plan_pages(int32_t B, int32_t page_size, int32_t num_pages, int32_t max_pages,
+                            int64_t table_stride, int32_t max_new_tokens, const int32_t* kept_len,
+                            const int32_t* n_new, const int32_t* held_in, int32_t* held_out,
+                            int32_t* free_pages, const int32_t* free_count_in,
+                            int32_t* free_count_out, int32_t* block_table, int32_t* q_start,
+                            int32_t* seq_len, int32_t* n_granted, int32_t* slot, int32_t* pos,
+                            int32_t* err_flag, void* stream);
+
+/*
+ * gva_paged_attention — attention of every request's new tokens, one or a chunk, over
+ * its pages: the absorbed route of gva_decode_attention and
+ * gva_decode_attention_multi (onedev.kr review, "How it works" and "What differs"),
+ * with a block table in place of a contiguous run of slots and a number of new tokens
+ * of its own for every request.  The new tokens are the last n = q_start[b+1] -
+ * q_start[b] of the request's seq_len[b] cached tokens (already appended); token i
+ * attends positions 0 .. seq_len[b] - n + i.  A token that this leaves nothing (its
+ * request counts fewer tokens than it brings) gets 0 and lse -inf.
+ *
+ *   q_abs      device [n_rows, H, d_h + d_r] float32 from gva_absorb_query (rows as q_start)
+ *   V_cache, kr_cache   device [num_slots, G, d_h] and [num_slots, d_r] cache_dtype;
+ *              num_slots a multiple of page_size, below 2^31 - 512 (kr_cache is ignored
+ *              if d_r == 0)
+ *   block_table   device [B, max_pages] int32, rows table_stride elements apart; only
+ *              the first ceil(seq_len / page_size) entries of a row are read
+ *   q_start    device [B + 1] int32, from 0, not decreasing, at most n_rows
+ *   seq_len    device [B] int32, counting the new tokens
+ *   max_query_len     host bound of a request's new tokens (sizes the workspace and
+ *              picks the kernels)
+ *   max_total_tokens  host bound of sum(seq_len) (sizes the split)
+ *   out, lse   device [n_rows, H, d_h] out_dtype and [n_rows, H] float32 or NULL, as
+ *              gva_decode_attention; rows of no request (from q_start[B] on) are left
+ *              as they were
+ *   workspace  zeroed once; gva_paged_workspace_size bytes; its first word is the
+ *              status word (GVA_DEVERR_*), as for gva_decode_attention.  Calls that may
+ *              overlap on the GPU (streams, or graphs) must use different workspaces.
+ * Slots behind a request's end may hold anything, NaN included.  On the device: a page
+ * id outside the cache, or a request longer than its table row, reads as 0 there and
+ * sets GVA_DEVERR_RANGE; a request whose row range is negative, leaves [0, n_rows) or
+ * exceeds max_query_len, or whose length is negative, is skipped and sets it too.
+ *
+ * Three kernels share the batch by new tokens per request:
+ *  - up to 8 query columns (new tokens * H/G) per value group: split-KV over all SMs on
+ *    mma.sync; bf16 cache, d_h in {32, 64, 128}, G in {2, 4, 8}, d_r <= 32;
+ *  - more: row blocks of 128 query rows on tcgen05, split over the keys as well where
+ *    there are few; bf16 cache, d_h in {64, 128}, d_r <= 32.  Probabilities are rounded
+ *    to bf16 before the value product when out is bf16, and split in two bf16 parts when
+ *    it is float32;
+ *  - every other shape (float32 caches, page sizes that are no multiple of 8, other
+ *    widths) on CUDA cores: right, but many times slower.
+ * Alignment: 16 bytes for every pointer except block_table, q_start and seq_len (4);
+ * cache rows (G*d_h*elt and d_r*elt) multiples of 16 bytes.
+ * Errors: GVA_ERR_INVALID_ARG, GVA_ERR_UNSUPPORTED, GVA_ERR_WORKSPACE, all before any
+ * launch.  B == 0 or n_rows == 0 is a no-op.
+ */
+size_t gva_paged_workspace_size(const gva_shape_t* shape, int32_t page_size, int32_t n_rows,
+                                int32_t max_query_len, int64_t max_total_tokens);
+
+gva_status_t gva_paged_attention(const gva_shape_t* shape, int32_t page_size, const float* q_abs,
+                                 const void* V_cache, const void* kr_cache, int64_t num_slots,
+                                 const int32_t* block_table, int32_t max_pages,
+                                 int64_t table_stride, const int32_t* q_start,
+                                 const int32_t* seq_len, int32_t n_rows, int32_t max_query_len,
+                                 int64_t max_total_tokens, void* out, float* lse, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/*
+ * gva_verify_draft — drafted tokens against the target model's probabilities, from
+ * given random numbers (speculative sampling), and the one token that follows them.
+ * The paper has no counterpart; gva_decode_attention_multi and gva_paged_attention
+ * compute the drafted tokens' attention, this call decides which of them stay.
+ *
+ * Request b was fed n = q_start[b+1] - q_start[b] tokens: its last token, then k = n-1
+ * drafts.  Row j of target_probs is the target's distribution of the token after fed
+ * token j, row j of draft_probs the one that draft was drawn from.  Draft x after row j
+ * is accepted, in order and until the first refusal, while
+ *     u_accept[j] * draft_probs[j][x] < target_probs[j][x]
+ * (draft_probs NULL: the drafts were not drawn, their probability is 1).  With a
+ * accepted, the token that follows has weights w = max(target - draft, 0) of row a
+ * after a refusal (target without x if draft_probs is NULL; target itself if that
+ * leaves nothing), w = target of row k when all are accepted; it is the first v with
+ *     w_0 + ... + w_v > u_sample[b] * sum(w),
+ * sums in 64 bits.  Weights that are not > 0, NaN included, count as 0; weights are
+ * otherwise finite.
+ *
+ *   vocab      > 0;  n_rows: rows of the buffers;  B in [0, 65535]
+ *   tokens     device [n_rows] int32: the fed tokens
+ *   q_start    device [B + 1] int32, as gva_paged_attention; a request may have no rows
+ *   target_probs, draft_probs   device [n_rows, vocab] probs_dtype, rows target_stride /
+ *              draft_stride (>= vocab) elements apart, no alignment beyond the element's
+ *   u_accept   device [n_rows] float32 in [0, 1);  u_sample device [B] float32 in [0, 1)
+ *   out_tokens device [n_rows] int32: the accepted drafts, then the new token, then -1,
+ *              from q_start[b]; rows of no request are left as they were
+ *   n_accepted device [B] int32: a (0 for a request without rows)
+ *   seq_len, kept_len   device [B] int32, both or neither: kept_len = seq_len - (k - a),
+ *              the cached tokens that stay (may be the same buffer)
+ *   err_flag   device int32 or NULL: GVA_DEVERR_RANGE is or-ed in by a draft outside
+ *              [0, vocab) (it counts as refused), a row without any probability (it
+ *              gives vocab - 1) or a row range outside [0, n_rows) (skipped)
+ * One launch, no workspace.  Errors: GVA_ERR_INVALID_ARG.  B == 0 is a no-op.
+ */
+gva_status_t gva_verify_draft(int32_t B, int32_t vocab, int32_t n_rows, const int32_t* tokens,
+                              const int32_t* q_start, int32_t probs_dtype,
+                              const void* target_probs, int64_t target_stride,
+                              const void* draft_probs, int64_t draft_stride,
+                              const float* u_accept, const float* u_sample, int32_t* out_tokens,
+                              int32_t* n_accepted, const int32_t* seq_len, int32_t* kept_len,
+                              int32_t* err_flag, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */
