@@ -37,7 +37,8 @@ struct PtCfg {
   // instructions), 64 with d_h = 64 (two CTAs per SM hide each other's hand-offs)
   static constexpr int TK = D_H == 128 && !HILO ? 128 : 64;
   static constexpr int CB = D_H / 64, KS = D_H / 16, RS = DRP / 16;
-  static constexpr int STAGES = (TK == 128 && D_H == 128) ? 2 : 3;
+  // two stages where a third would cost the second CTA of an SM (or not fit)
+  static constexpr int STAGES = (TK == 128 || (D_H == 64 && DRP == 32 && !HILO)) ? 2 : 3;
   static constexpr int QB = M * D_H * 2;     // q~ hi (or lo): CB blocks of M rows x 128 B
   static constexpr int QRB = DRP ? (M * DRP * 2 + 1023) / 1024 * 1024 : 0;
   static constexpr int PH = M * TK * 2;      // one half of P: TK/64 blocks of M rows x 128 B
@@ -316,18 +317,22 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           tc::fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free + 8 * pb);
-          float mx = -INFINITY;
+          // four running maxima (and sums below): one chain of 64 dependent operations
+          // would cost more than the operations themselves
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           if (ok && t0 + C::TK <= kv_all) {   // every row sees the whole tile: no mask
 #pragma unroll
-            for (int j = 0; j < C::TK; ++j) mx = fmaxf(mx, x[j]);
+            for (int j = 0; j < C::TK; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], x[j]);
           } else {
+            // columns [0, vis) of this row count
+            const int vis = ok && valid ? min(lim + 1, s.L) - t0 : 0;
 #pragma unroll
             for (int j = 0; j < C::TK; ++j) {
-              const bool vis = ok && valid && t0 + j <= lim && t0 + j < s.L;
-              x[j] = vis ? x[j] : -INFINITY;
-              mx = fmaxf(mx, x[j]);
+              x[j] = j < vis ? x[j] : -INFINITY;
+              mx4[j & 3] = fmaxf(mx4[j & 3], x[j]);
             }
           }
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           // a row keeps the maximum its exponentials are taken against until a tile
           // exceeds it by more than 8 (log2 units): P <= 2^8, and O is touched only then
           const bool grow = mx > m + 8.f;
@@ -338,14 +343,14 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
             ok = ok && mbar_wait(pv_done + 8 * pb, ((kk - 2) >> 1) & 1, a.status);
             tc::fence_after();
           }
-          float rsum = 0.f;
+          float rs4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < C::TK / 8; ++c) {
             float e[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               e[i] = ex2(x[8 * c + i] - ms);
-              rsum += e[i];
+              rs4[i & 3] += e[i];
             }
             const uint32_t o = (c >> 3) * (C::M * 128) + sw128(r, c & 7);
             if constexpr (C::HILO) {
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
                                                                pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
             }
           }
-          l = l * alpha + rsum;
+          l = l * alpha + ((rs4[0] + rs4[1]) + (rs4[2] + rs4[3]));
           m = mn;
         }
         // value rows behind the sequence meet P = 0 but may hold anything (NaN): zero

@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kPlanMaxThreads = 1024;
 constexpr int kPlanPer = kMaxBatch / kPlanMaxThreads;   // requests per thread at most
+constexpr int kTok = 4;                                 // new tokens per thread in flight
 
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -54,19 +55,21 @@ __device__ __forceinline__ void scan_pair(long long& x, long long& y, long long&
   }
   if (lane == 31) tmp[w] = make_longlong2(ix, iy);
   __syncthreads();
-  long long bx = 0, by = 0;
-  tx = ty = 0;
-  for (int u = 0; u < nw; ++u) {
-    const longlong2 s = tmp[u];
-    if (u < w) {
-      bx += s.x;
-      by += s.y;
+  // every warp scans the warps' sums, one per lane
+  const longlong2 s = lane < nw ? tmp[lane] : make_longlong2(0, 0);
+  long long bx = s.x, by = s.y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long ux = __shfl_up_sync(0xffffffffu, bx, o), uy = __shfl_up_sync(0xffffffffu, by, o);
+    if (lane >= o) {
+      bx += ux;
+      by += uy;
     }
-    tx += s.x;
-    ty += s.y;
   }
-  x = bx + ix - x;
-  y = by + iy - y;
+  tx = __shfl_sync(0xffffffffu, bx, 31);
+  ty = __shfl_sync(0xffffffffu, by, 31);
+  x = __shfl_sync(0xffffffffu, bx - s.x, w) + ix - x;
+  y = __shfl_sync(0xffffffffu, by - s.y, w) + iy - y;
   __syncthreads();   // tmp free again
 }
 
@@ -213,19 +216,31 @@ __global__ void __launch_bounds__(kPlanMaxThreads) plan_pages_kernel(const PlanA
     const int idx = (int)(top - 1 - r);
     return idx < count ? a.free_pages[idx] : returned(idx - count);
   };
-  for (int i = gid; i < a.max_new; i += gt) {
-    int sl = -1, p = -1;
-    if (i < n_tokens) {
-      const int b = owner_of(qs, B, i);
-      p = kept[b] + (i - qs[b]);
-      const int col = p / a.page;
-      const int pg = col < held[b] ? a.table[(long long)b * a.table_stride + col]
-                                   : page_of_rank(np[b] + col - held[b]);
-      if (pg >= 0 && pg < a.num_pages) sl = pg * a.page + p % a.page;
-      else if (a.err_flag) atomicOr(a.err_flag, GVA_DEVERR_RANGE);
+  // Tokens, kTok per thread at a time: their searches and table reads are independent
+  // chains that overlap.
+  for (int i0 = gid; i0 < a.max_new; i0 += kTok * gt) {
+    int p[kTok], pg[kTok];
+#pragma unroll
+    for (int u = 0; u < kTok; ++u) {
+      const int i = i0 + u * gt;
+      p[u] = pg[u] = -1;
+      if (i < n_tokens) {
+        const int b = owner_of(qs, B, i);
+        p[u] = kept[b] + (i - qs[b]);
+        const int col = p[u] / a.page;
+        pg[u] = col < held[b] ? a.table[(long long)b * a.table_stride + col]
+                              : page_of_rank(np[b] + col - held[b]);
+      }
     }
-    a.slot[i] = sl;
-    a.pos[i] = p;
+#pragma unroll
+    for (int u = 0; u < kTok; ++u) {
+      const int i = i0 + u * gt;
+      if (i >= a.max_new) break;
+      const bool ok = pg[u] >= 0 && pg[u] < a.num_pages;
+      if (!ok && i < n_tokens && a.err_flag) atomicOr(a.err_flag, GVA_DEVERR_RANGE);
+      a.slot[i] = ok ? pg[u] * a.page + p[u] % a.page : -1;
+      a.pos[i] = p[u];
+    }
   }
   for (int k = gid; k < n_back; k += gt) a.free_pages[count + k] = returned(k);
   for (int r = gid; r < n_pages; r += gt) {

@@ -13,9 +13,9 @@
 //
 // What bounds it: memory.  Besides k probabilities a request reads one row of each
 // model, vocab * 2 * 4 bytes, once.  A cluster of CTAs shares a request: each warp
-// sums a contiguous chunk (16-byte loads, four in flight per row and lane), the
-// chunk sums meet through distributed shared memory, and the one warp whose chunk
-// holds the answer reads it again from L2.
+// sums a contiguous chunk (16-byte loads, two in flight per row and lane, four CTAs per SM), the
+// chunk sums meet through distributed shared memory, and the CTA whose chunk
+// holds the answer reads it again from L2, an eighth per warp.
 // Sums are in 64 bits: with ~10^5 tokens of mass ~10^-5 each, 32-bit running sums
 // are off by a good part of a token's mass, and the drawn token would depend on the
 // order of the additions.
@@ -30,7 +30,7 @@ namespace {
 constexpr int kVfWarps = 8;
 constexpr int kVfThreads = 32 * kVfWarps;
 constexpr int kVfMaxCluster = 8;
-constexpr int kVfUnroll = 4;   // 16-byte vectors in flight per lane and row
+constexpr int kVfUnroll = 2;   // 16-byte vectors in flight per lane and row
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -182,7 +182,7 @@ __device__ __forceinline__ int chunk_find(const Weights<T>& W, int v0, int v1, d
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyArgs a, const int cl) {
+__global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs a, const int cl) {
   __shared__ double sums[kVfWarps];
   __shared__ double all[kVfMaxCluster * kVfWarps];
   __shared__ int s_first;
@@ -286,9 +286,32 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyArgs a, 
         ch = __shfl_sync(0xffffffffu, s1 > 0.0 ? 2 * lane + 1 : 2 * lane, l);
         base = __shfl_sync(0xffffffffu, s1 > 0.0 ? e1 : e0, l);
       }
-      if (ch == c) {
-        token = chunk_find(W, edge(c), edge(c + 1), base, t, lane);
-        found = true;
+      if (ch >= 0 && ch / kVfWarps == (int)rank) {
+        // this CTA's warps share the chunk once more: sums of its eighths (from L2),
+        // then the one warp whose eighth holds the answer walks it
+        const int v0 = edge(ch), sub = (len / kVfWarps + SEG - 1) / SEG * SEG, v1 = edge(ch + 1);
+        const int w0 = min(v0 + warp * sub, v1), w1 = min(v0 + (warp + 1) * sub, v1);
+        const double sw = chunk_sum(W, w0, w1, lane);
+        if (lane == 0) sums[warp] = sw;
+        __syncthreads();
+        int at = -1, last = -1;
+        double run = base, from = base;
+        for (int w = 0; w < kVfWarps; ++w) {
+          const double x = sums[w];
+          if (x > 0.0) {
+            last = w;
+            if (at < 0) {
+              from = run;
+              if (run + x > t) at = w;
+            }
+          }
+          run += x;
+        }
+        if (at < 0) at = last;
+        if (warp == at) {
+          token = chunk_find(W, w0, w1, from, t, lane);
+          found = true;
+        }
       } else if (ch < 0 && c == 0) {   // a row without any probability
         token = a.vocab - 1;
         found = true;
@@ -316,7 +339,7 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyArgs a, 
 
 cudaError_t launch_verify(const VerifyArgs& a, bool bf16, int num_sms, cudaStream_t st) {
   int cl = kVfMaxCluster;
-  while (cl > 1 && (long long)a.B * cl > 8ll * num_sms) cl >>= 1;
+  while (cl > 1 && (long long)a.B * cl > 4ll * num_sms) cl >>= 1;   // one wave of CTAs
   static_assert(kVfMaxCluster * kVfWarps <= 64, "two chunk sums per lane");
   const dim3 grid((unsigned)(a.B * cl)), block(kVfThreads);
   if (bf16) return launch_pdl_cluster(verify_kernel<__nv_bfloat16>, grid, block, cl, 0, st, a, cl);
