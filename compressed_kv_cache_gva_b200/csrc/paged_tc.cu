@@ -17,9 +17,13 @@
 //
 // Roles: warp 0 streams tiles with 2-D TMA loads, one box per page (or part of one),
 // its lanes holding the cache rows of the next 32 boxes; one thread of warp 1 issues
-// every MMA; warps 4..7 (a TMEM lane quarter each) do the softmax, write P to shared
-// memory and rescale O only when a row's maximum grew by more than 2^8.  All ring and
-// buffer barriers count tiles over the whole CTA, so they run on across pieces.
+// every MMA; warps 4..7 (a TMEM lane quarter each) do the softmax, write P back to
+// tensor memory (the A operand of the value product) and rescale O only when a row's
+// maximum grew by more than 2^8.  While they exponentiate tile k, the MMA thread has
+// the scores of tile k + 1 computed.  All ring and buffer barriers count tiles over the
+// whole CTA, so they run on across pieces.
+#include <atomic>
+
 #include "launch.h"
 #include "paged.cuh"
 #include "tc.cuh"
@@ -33,35 +37,41 @@ struct PtCfg {
   static constexpr int D_H = D_H_, DRP = DRP_;
   static constexpr bool HILO = HILO_;        // P in two bf16 halves (float32 output)
   static constexpr int M = kPagedTcRows;
-  // keys per tile: 128 with d_h = 128 (one CTA per SM either way, half the score
-  // instructions), 64 with d_h = 64 (two CTAs per SM hide each other's hand-offs)
-  static constexpr int TK = D_H == 128 && !HILO ? 128 : 64;
+  // Keys per tile.  S, P and O of two CTAs share the SM's 512 tensor-memory columns:
+  // 128 + 64 + 64 with d_h = 64, 64 + 32 + 128 with d_h = 128, 64 + 64 + d_h where P
+  // has two halves.  Longer tiles have fewer hand-offs per key.
+  static constexpr int TK = D_H == 64 && !HILO ? 128 : 64;
   static constexpr int CB = D_H / 64, KS = D_H / 16, RS = DRP / 16;
-  // two stages where a third would cost the second CTA of an SM (or not fit)
-  static constexpr int STAGES = (TK == 128 || (D_H == 64 && DRP == 32 && !HILO)) ? 2 : 3;
   static constexpr int QB = M * D_H * 2;     // q~ hi (or lo): CB blocks of M rows x 128 B
   static constexpr int QRB = DRP ? (M * DRP * 2 + 1023) / 1024 * 1024 : 0;
-  static constexpr int PH = M * TK * 2;      // one half of P: TK/64 blocks of M rows x 128 B
-  static constexpr int PB = HILO ? 2 * PH : PH;
   static constexpr int VB = CB * TK * 128;
   static constexpr int KRB = DRP * TK * 2;
   static constexpr int STAGE = VB + (KRB + 1023) / 1024 * 1024;
-  static constexpr int OFF_QR = 2 * QB, OFF_P = OFF_QR + 2 * QRB, OFF_RING = OFF_P + 2 * PB;
+  static constexpr int OFF_QR = 2 * QB, OFF_RING = OFF_QR + 2 * QRB;
+  // as many stages as let two CTAs share an SM, or one where not even two stages fit
+  static constexpr int HALF = 113 * 1024 - 2048, WHOLE = 227 * 1024 - 2048;
+  static constexpr bool TWO = OFF_RING + 2 * STAGE <= HALF;
+  static constexpr int STAGES_RAW = ((TWO ? HALF : WHOLE) - OFF_RING) / STAGE;
+  static constexpr int STAGES = STAGES_RAW > 6 ? 6 : STAGES_RAW;
+  static constexpr int PER_SM = TWO ? 2 : 1;
   static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
-  // full[S], empty[S], s_full[2], s_free[2], p_full[2], pv_done[2], fin
-  static constexpr int NBAR = 2 * STAGES + 9;
-  // the unit prefix of the prologue lies where P goes later
+  // full[S], empty[S], s_full, s_free, p_full, pv_done, fin
+  static constexpr int NBAR = 2 * STAGES + 5;
+  // the unit prefix of the prologue lies where the ring is later
   static constexpr int SMEM = 1024 + OFF_BAR + NBAR * 8 + 8;
-  static constexpr uint32_t S_COL = 0, O_COL = 2 * TK;
-  static constexpr uint32_t TMEM_COLS = O_COL + D_H > 256 ? 512 : 256;
+  static_assert(STAGES * STAGE >= (int)sizeof(int) * (kMaxBatch + 1) + 16 + 33 * 8, "unit prefix");
+  static_assert(STAGES >= 2 && SMEM <= 227 * 1024, "shared memory");
+  static constexpr uint32_t S_COL = 0, P_COL = TK, P_COLS = TK / 2;
+  static constexpr uint32_t O_COL = D_H == 64 && !HILO ? 192 : 128;
+  static constexpr uint32_t TMEM_COLS = 256;
+  static_assert(P_COL + P_COLS * (HILO ? 2 : 1) <= O_COL && O_COL + D_H <= TMEM_COLS, "tensor memory");
   static constexpr uint32_t TX = VB + KRB;
   static constexpr int THREADS = 256;
   static constexpr uint32_t SW_R = DRP == 32 ? tc::kSw64 : tc::kSw32;
   static constexpr uint32_t SBO_R = DRP * 2 * 8;
-  // CTAs per SM that shared and tensor memory hold: registers are budgeted for them
-  static constexpr int PER_SM = 2 * (SMEM + 1024) <= 227 * 1024 && 2 * TMEM_COLS <= 512 ? 2 : 1;
-  static_assert(2 * PB >= (int)sizeof(int) * (kMaxBatch + 1) + 16 + 33 * 8, "unit prefix");
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  // A row of 128 scores does not fit the 128 registers that two CTAs leave a thread:
+  // the softmax warps take theirs from the other four (72 + 184 = 2 x 128)
+  static constexpr bool SPLIT_REGS = TK == 128 && PER_SM == 2;
 };
 
 // 16-byte chunk of a row in a swizzled K-major tile (rows of 128, 64 or 32 bytes).
@@ -86,6 +96,61 @@ __device__ __forceinline__ uint4 split_bf16(const float* x, uint4& lo) {
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
+// Two packed fp32 additions (one instruction on sm_100).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Queries of a piece -> shared memory: bf16 hi and lo halves, swizzled K-major rows.
+template <class C>
+__device__ __forceinline__ void load_queries(const PagedArgs& a, const RowPiece& p, const SeqRows& s,
+                                             uint8_t* sm) {
+  const int hpr = a.hpr, dq = C::D_H + a.d_r, row0 = p.rb * C::M, rows = min(C::M, s.n * hpr - row0);
+#pragma unroll 2
+  for (int e = threadIdx.x; e < C::M * (C::D_H / 8); e += C::THREADS) {
+    const int r = e / (C::D_H / 8), c = e % (C::D_H / 8);
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (r < rows) {
+      const int R = row0 + r;
+      const float* src = a.q_abs + ((long long)(s.r0 + R / hpr) * a.H + p.g * hpr + R % hpr) * dq + c * 8;
+      const float4 u = *reinterpret_cast<const float4*>(src);
+      const float4 v = *reinterpret_cast<const float4*>(src + 4);
+      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+      x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    }
+    uint4 lo;
+    const uint4 hi = split_bf16(x, lo);
+    const uint32_t o = (c / 8) * (C::M * 128) + sw128(r, c % 8);
+    *reinterpret_cast<uint4*>(sm + o) = hi;
+    *reinterpret_cast<uint4*>(sm + o + C::QB) = lo;
+  }
+  if constexpr (C::DRP > 0) {
+    for (int e = threadIdx.x; e < C::M * (C::DRP / 8); e += C::THREADS) {
+      const int r = e / (C::DRP / 8), c = e % (C::DRP / 8), R = row0 + r;
+      const float* src = a.q_abs + ((long long)(s.r0 + R / hpr) * a.H + p.g * hpr + R % hpr) * dq + C::D_H;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = (r < rows && c * 8 + i < a.d_r) ? src[c * 8 + i] : 0.f;
+      uint4 lo;
+      const uint4 hi = split_bf16(x, lo);
+      const uint32_t o = C::OFF_QR + sw_pos<C::DRP>(r, c);
+      *reinterpret_cast<uint4*>(sm + o) = hi;
+      *reinterpret_cast<uint4*>(sm + o + C::QRB) = lo;
+    }
+  }
+  fence_proxy_async_smem();   // the queries are read by the tensor core (async proxy)
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     paged_tc_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tm_v,
@@ -95,10 +160,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   const uint32_t sb = smem_u32(sm);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   const uint32_t full = smem_u32(bars), empty = full + 8 * C::STAGES;
-  const uint32_t s_full = empty + 8 * C::STAGES, s_free = s_full + 16;
-  const uint32_t p_full = s_free + 16, pv_done = p_full + 16, fin = pv_done + 16;
+  const uint32_t s_full = empty + 8 * C::STAGES, s_free = s_full + 8;
+  const uint32_t p_full = s_free + 8, pv_done = p_full + 8, fin = pv_done + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
-  int* prefix = reinterpret_cast<int*>(sm + C::OFF_P);
+  int* prefix = reinterpret_cast<int*>(sm + C::OFF_RING);
   long long* wtmp = reinterpret_cast<long long*>(
       (reinterpret_cast<uintptr_t>(prefix + a.B + 1) + 15) & ~uintptr_t(15));
   __shared__ RowPiece piece;
@@ -110,12 +175,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + 8 * i, 1);
-      mbar_init(s_free + 8 * i, 4);
-      mbar_init(p_full + 8 * i, 4);
-      mbar_init(pv_done + 8 * i, 1);
-    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 4);
+    mbar_init(p_full, 4);
+    mbar_init(pv_done, 1);
     mbar_init(fin, 1);
     fence_barrier_init();
   }
@@ -147,99 +210,67 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // kt: tiles of this CTA before the piece; all barrier phases count from it
-  int kt = 0, issued = 0;
-  bool ok = true;   // false once a bounded wait gave up: skip work, keep the order
-  while (more) {
-    const RowPiece p = piece;
-    const SeqRows s = seq_rows(a, p.b);
-    const int row0 = p.rb * C::M, rows = min(C::M, s.n * hpr - row0);
-    const int nk = p.k1 - p.k0;
-
-    // ---- queries -> shared memory: bf16 hi and lo halves, swizzled K-major rows
-    const int dq = C::D_H + a.d_r;
-    for (int e = threadIdx.x; e < C::M * (C::D_H / 8); e += C::THREADS) {
-      const int r = e / (C::D_H / 8), c = e % (C::D_H / 8);
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (r < rows) {
-        const int R = row0 + r;
-        const float* src = a.q_abs + ((long long)(s.r0 + R / hpr) * a.H + p.g * hpr + R % hpr) * dq + c * 8;
-        const float4 u = *reinterpret_cast<const float4*>(src);
-        const float4 v = *reinterpret_cast<const float4*>(src + 4);
-        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-      }
-      uint4 lo;
-      const uint4 hi = split_bf16(x, lo);
-      const uint32_t o = (c / 8) * (C::M * 128) + sw128(r, c % 8);
-      *reinterpret_cast<uint4*>(sm + o) = hi;
-      *reinterpret_cast<uint4*>(sm + o + C::QB) = lo;
-    }
-    if constexpr (C::DRP > 0) {
-      for (int e = threadIdx.x; e < C::M * (C::DRP / 8); e += C::THREADS) {
-        const int r = e / (C::DRP / 8), c = e % (C::DRP / 8), R = row0 + r;
-        const float* src = a.q_abs + ((long long)(s.r0 + R / hpr) * a.H + p.g * hpr + R % hpr) * dq + C::D_H;
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (r < rows && c * 8 + i < a.d_r) ? src[c * 8 + i] : 0.f;
-        uint4 lo;
-        const uint4 hi = split_bf16(x, lo);
-        const uint32_t o = C::OFF_QR + sw_pos<C::DRP>(r, c);
-        *reinterpret_cast<uint4*>(sm + o) = hi;
-        *reinterpret_cast<uint4*>(sm + o + C::QRB) = lo;
-      }
-    }
-    fence_proxy_async_smem();   // the queries are read by the tensor core (async proxy)
-    __syncthreads();
-
-    if (warp == 0) {
-      // ---------------------------------------------------------- producer
-      const int per_tile = C::TK >> a.box_log2;
-      const int* row = a.table + (long long)p.b * a.table_stride;
-      int base = p.k0 * per_tile;
-      const int end = p.k1 * per_tile;
-      auto look = [&](int i) { return i < end ? slot_of(a, row, i << a.box_log2, s.L) : a.num_slots; };
-      int y_now = look(base + lane), y_next = look(base + 32 + lane);
-      for (int k = 0; k < nk; ++k) {
-        const int box0 = (p.k0 + k) * per_tile;
-        if (box0 - base >= 32) {
-          base += 32;
-          y_now = y_next;
-          y_next = look(base + 32 + lane);
-        }
-        const int kk = kt + k, sg = kk % C::STAGES;
-        if (ok && kk >= C::STAGES) ok = mbar_wait(empty + 8 * sg, ((kk / C::STAGES) - 1) & 1, a.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t fb = full + 8 * sg, st = sb + C::OFF_RING + sg * C::STAGE;
-        if (lane == 0) mbar_arrive_expect_tx(fb, C::TX);
-        __syncwarp();
-        for (int j = 0; j < per_tile; ++j) {
-          const int y = __shfl_sync(0xffffffffu, y_now, box0 + j - base);
-          if (lane == 0) {
-            const uint32_t r = (uint32_t)j << a.box_log2;
-#pragma unroll
-            for (int c = 0; c < C::CB; ++c)
-              tma_load_2d(st + c * C::TK * 128 + r * 128, &tm_v, p.g * C::D_H + c * 64, y, fb);
-            if constexpr (C::DRP > 0) tma_load_2d(st + C::VB + r * C::DRP * 2, &tm_kr, 0, y, fb);
+  // kt: tiles of this CTA before the piece; all barrier phases count from it.
+  // ok: false once a bounded wait gave up: skip work, keep the order.
+  // Both halves of the CTA walk the same pieces: load the queries, barrier, their
+  // roles, barrier.
+  int kt = 0;
+  bool ok = true;
+  if (warp < 4) {
+    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    int issued = 0;
+    while (more) {
+      const RowPiece p = piece;
+      const SeqRows s = seq_rows(a, p.b);
+      const int nk = p.k1 - p.k0;
+      load_queries<C>(a, p, s, sm);
+      __syncthreads();
+      if (warp == 0) {
+        // -------------------------------------------------------- producer
+        const int per_tile = C::TK >> a.box_log2;
+        const int* row = a.table + (long long)p.b * a.table_stride;
+        int base = p.k0 * per_tile;
+        const int end = p.k1 * per_tile;
+        auto look = [&](int i) { return i < end ? slot_of(a, row, i << a.box_log2, s.L) : a.num_slots; };
+        int y_now = look(base + lane), y_next = look(base + 32 + lane);
+        for (int k = 0; k < nk; ++k) {
+          const int box0 = (p.k0 + k) * per_tile;
+          if (box0 - base >= 32) {
+            base += 32;
+            y_now = y_next;
+            y_next = look(base + 32 + lane);
           }
+          const int kk = kt + k, sg = kk % C::STAGES;
+          if (ok && kk >= C::STAGES) ok = mbar_wait(empty + 8 * sg, ((kk / C::STAGES) - 1) & 1, a.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t fb = full + 8 * sg, st = sb + C::OFF_RING + sg * C::STAGE;
+          if (lane == 0) mbar_arrive_expect_tx(fb, C::TX);
+          __syncwarp();
+          for (int j = 0; j < per_tile; ++j) {
+            const int y = __shfl_sync(0xffffffffu, y_now, box0 + j - base);
+            if (lane == 0) {
+              const uint32_t r = (uint32_t)j << a.box_log2;
+#pragma unroll
+              for (int c = 0; c < C::CB; ++c)
+                tma_load_2d(st + c * C::TK * 128 + r * 128, &tm_v, p.g * C::D_H + c * 64, y, fb);
+              if constexpr (C::DRP > 0) tma_load_2d(st + C::VB + r * C::DRP * 2, &tm_kr, 0, y, fb);
+            }
+          }
+          issued = kk + 1;
         }
-        issued = kk + 1;
-      }
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issue
-      if (lane == 0) {
+      } else if (warp == 1 && lane == 0) {
+        // -------------------------------------------------------- MMA issue
         constexpr uint32_t idS = tc::idesc_bf16(C::M, C::TK, 0, 0);   // Q (K-major) x V^T (K-major)
-        constexpr uint32_t idO = tc::idesc_bf16(C::M, C::D_H, 0, 1);  // P (K-major) x V (MN-major)
+        constexpr uint32_t idO = tc::idesc_bf16(C::M, C::D_H, 0, 1);  // P (tensor memory) x V (MN-major)
         for (int k = 0; k <= nk; ++k) {
           if (k < nk) {
             const int kk = kt + k, sg = kk % C::STAGES;
             ok = ok && mbar_wait(full + 8 * sg, (kk / C::STAGES) & 1, a.status);
-            if (kk >= 2) ok = ok && mbar_wait(s_free + 8 * (kk & 1), ((kk - 2) >> 1) & 1, a.status);
+            if (kk >= 1) ok = ok && mbar_wait(s_free, (kk - 1) & 1, a.status);
             tc::fence_after();
             if (ok) {
-              const uint32_t d = tmem + C::S_COL + (kk & 1) * C::TK;
-              const uint32_t vt = sb + C::OFF_RING + sg * C::STAGE;
+              const uint32_t d = tmem + C::S_COL, vt = sb + C::OFF_RING + sg * C::STAGE;
 #pragma unroll
               for (int ks = 0; ks < C::KS; ++ks) {
                 const uint32_t kb = (ks >> 2) * (C::M * 128) + (ks & 3) * 32;
@@ -256,114 +287,146 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
                              idS, 1);
               }
             }
-            tc::commit(s_full + 8 * (kk & 1));
+            tc::commit(s_full);
           }
           if (k >= 1) {   // P.V of the tile before
-            const int kp = kt + k - 1, sp = kp % C::STAGES, pb = kp & 1;
-            ok = ok && mbar_wait(p_full + 8 * pb, (kp >> 1) & 1, a.status);
+            const int kp = kt + k - 1, sp = kp % C::STAGES;
+            ok = ok && mbar_wait(p_full, kp & 1, a.status);
             tc::fence_after();
             if (ok) {
               const uint32_t vt = sb + C::OFF_RING + sp * C::STAGE;
 #pragma unroll
-              for (int h = 0; h < (C::HILO ? 2 : 1); ++h) {
-                const uint32_t pt = sb + C::OFF_P + pb * C::PB + h * C::PH;
+              for (int h = 0; h < (C::HILO ? 2 : 1); ++h)
 #pragma unroll
                 for (int kk = 0; kk < C::TK / 16; ++kk)
-                  tc::mma_bf16(tmem + C::O_COL,
-                               tc::smem_desc(pt + (kk >> 2) * (C::M * 128) + (kk & 3) * 32, 16, 1024,
-                                             tc::kSw128),
-                               tc::smem_desc(vt + kk * 16 * 128, C::TK * 128, 1024, tc::kSw128), idO,
-                               (k > 1 || h > 0 || kk > 0) ? 1u : 0u);
-              }
+                  tc::mma_bf16_ts(tmem + C::O_COL, tmem + C::P_COL + h * C::P_COLS + kk * 8,
+                                  tc::smem_desc(vt + kk * 16 * 128, C::TK * 128, 1024, tc::kSw128), idO,
+                                  (k > 1 || h > 0 || kk > 0) ? 1u : 0u);
             }
-            tc::commit(pv_done + 8 * pb);
+            tc::commit(pv_done);
             tc::commit(empty + 8 * sp);
           }
         }
       }
-    } else if (warp >= 4) {
+      __syncwarp();   // the issuing lanes rejoin their warps before the barrier
+      kt += nk;
+      if (threadIdx.x == 0) {
+        if (p.k0 == 0 && nk < p.nt)   // started here, ended elsewhere: where its pieces are
+          a.meta[blockIdx.x] = make_int4(ts.cta_of(walk.u + p.nt - 1) - (int)blockIdx.x + 1, p.b, p.g, p.rb);
+        more = walk.next();
+        piece = walk.p;
+      }
+      __syncwarp();
+      __syncthreads();   // all roles are done with the piece; the next one's is in place
+      tc::fence_after();
+    }
+    // ---- nothing in flight may outlive the CTA: copies, then MMAs
+    if (warp == 0 && lane == 0) {
+      for (int kk = max(0, issued - C::STAGES); kk < issued; ++kk)
+        mbar_wait(full + 8 * (kk % C::STAGES), (kk / C::STAGES) & 1, a.status);
+    }
+    if (warp == 1 && lane == 0) {
+      tc::commit(fin);
+      mbar_wait(fin, 0, a.status);
+    }
+    __syncwarp();
+  } else {
+    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    const int quarter = warp & 3, r = 32 * quarter + lane;
+    const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
+    while (more) {
+      const RowPiece p = piece;
+      const SeqRows s = seq_rows(a, p.b);
+      const int nk = p.k1 - p.k0, row0 = p.rb * C::M, rows = min(C::M, s.n * hpr - row0);
+      load_queries<C>(a, p, s, sm);
+      __syncthreads();
       // ---------------------------------------------------------- softmax, P, O rescale, output
-      const int quarter = warp & 3, r = 32 * quarter + lane;
-      const bool valid = r < rows, idle = 32 * quarter >= rows;   // idle: no row of this warp counts
+      // idle: no row of this warp counts.  A row of P meets only its own row of O, so
+      // what idle lanes of the tensor memory hold does not matter.
+      const bool valid = r < rows, idle = 32 * quarter >= rows;
       const int R = row0 + r, qi = R / hpr, head = p.g * hpr + R % hpr;
       const int lim = s.L - s.n + qi;                             // last key of this row
       const int kv_all = s.L - s.n + row0 / hpr + 1;              // keys every row sees
-      const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < nk; ++k) {
-        const int kk = kt + k, pb = kk & 1, t0 = (p.k0 + k) * C::TK;
-        ok = ok && mbar_wait(s_full + 8 * pb, (kk >> 1) & 1, a.status);
+        const int kk = kt + k, t0 = (p.k0 + k) * C::TK;
+        ok = ok && mbar_wait(s_full, kk & 1, a.status);
         tc::fence_after();
-        float x[C::TK];
-        float alpha = 1.f;
-        uint8_t* prow = sm + C::OFF_P + pb * C::PB;
-        if (idle) {
-          // rows past the block: their P only has to be finite (their O is never read)
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free + 8 * pb);
-          if (kk >= 2) {
-            ok = ok && mbar_wait(pv_done + 8 * pb, ((kk - 2) >> 1) & 1, a.status);
-            tc::fence_after();
-          }
-          if (k < 2) {
+        if (!idle) {
+          float x[C::TK];
 #pragma unroll
-            for (int c = 0; c < C::PB / (C::M * 16); ++c)
-              *reinterpret_cast<uint4*>(prow + (c >> 3) * (C::M * 128) + sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
-          }
-        } else {
-#pragma unroll
-          for (int q4 = 0; q4 < C::TK / 16; ++q4) tc::ld16(trow + C::S_COL + pb * C::TK + q4 * 16, x + q4 * 16);
+          for (int q = 0; q < C::TK / 32; ++q) tc::ld32(trow + C::S_COL + q * 32, x + q * 32);
           tc::wait_ld();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(s_free + 8 * pb);
-          // four running maxima (and sums below): one chain of 64 dependent operations
-          // would cost more than the operations themselves
+          if (lane == 0) mbar_arrive(s_free);
+          // four running maxima (and sums below): one dependent chain would cost more
+          // than the operations themselves
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if (ok && t0 + C::TK <= kv_all) {   // every row sees the whole tile: no mask
-#pragma unroll
-            for (int j = 0; j < C::TK; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], x[j]);
-          } else {
-            // columns [0, vis) of this row count
+          if (!ok || t0 + C::TK > kv_all) {   // some row does not see the whole tile
             const int vis = ok && valid ? min(lim + 1, s.L) - t0 : 0;
 #pragma unroll
-            for (int j = 0; j < C::TK; ++j) {
-              x[j] = j < vis ? x[j] : -INFINITY;
-              mx4[j & 3] = fmaxf(mx4[j & 3], x[j]);
-            }
+            for (int j = 0; j < C::TK; ++j) x[j] = j < vis ? x[j] : -INFINITY;
           }
+#pragma unroll
+          for (int j = 0; j < C::TK; j += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx4[i] = max3(mx4[i], x[j + 2 * i], x[j + 2 * i + 1]);
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           // a row keeps the maximum its exponentials are taken against until a tile
           // exceeds it by more than 8 (log2 units): P <= 2^8, and O is touched only then
           const bool grow = mx > m + 8.f;
           const float mn = grow ? mx : m;
           const float ms = mn == -INFINITY ? 0.f : mn;
-          alpha = ex2(m - ms);
-          if (kk >= 2) {   // P buffer free: the P.V of two tiles ago has completed
-            ok = ok && mbar_wait(pv_done + 8 * pb, ((kk - 2) >> 1) & 1, a.status);
-            tc::fence_after();
-          }
-          float rs4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < C::TK / 8; ++c) {
-            float e[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              e[i] = ex2(x[8 * c + i] - ms);
-              rs4[i & 3] += e[i];
-            }
-            const uint32_t o = (c >> 3) * (C::M * 128) + sw128(r, c & 7);
-            if constexpr (C::HILO) {
-              uint4 lo;
-              *reinterpret_cast<uint4*>(prow + o) = split_bf16(e, lo);
-              *reinterpret_cast<uint4*>(prow + C::PH + o) = lo;
-            } else {
-              *reinterpret_cast<uint4*>(prow + o) = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
-                                                               pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
-            }
-          }
-          l = l * alpha + ((rs4[0] + rs4[1]) + (rs4[2] + rs4[3]));
+          const float alpha = ex2(m - ms);
           m = mn;
+          const float2 neg = make_float2(-ms, -ms);
+          float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+          for (int q = 0; q < C::TK / 32; ++q) {   // 32 keys at a time
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 e = add2(make_float2(x[32 * q + 2 * i], x[32 * q + 2 * i + 1]), neg);
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              sum[i & 3] = add2(sum[i & 3], e);
+              if constexpr (C::HILO) {
+                const float hx = bf16_round(e.x), hy = bf16_round(e.y);
+                hi[i] = pack_bf16(hx, hy);
+                lo[i] = pack_bf16(e.x - hx, e.y - hy);
+              } else {
+                hi[i] = pack_bf16(e.x, e.y);
+              }
+            }
+            if (q == 0 && kk >= 1) {   // P is free, and O still, once the P.V before has completed
+              ok = ok && mbar_wait(pv_done, (kk - 1) & 1, a.status);
+              tc::fence_after();
+            }
+            tc::st16u(trow + C::P_COL + q * 16, hi);
+            if constexpr (C::HILO) tc::st16u(trow + C::P_COL + C::P_COLS + q * 16, lo);
+          }
+          l = l * alpha + (((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
+                           ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y)));
+          // O *= alpha before this tile's P.V
+          if (k >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+            for (int q4 = 0; q4 < C::D_H / 16; ++q4) {
+              float o[16];
+              tc::ld16(trow + C::O_COL + q4 * 16, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= alpha;
+              tc::st16(trow + C::O_COL + q4 * 16, o);
+            }
+          }
+          tc::wait_st();
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+          // keep step with the warps that write P: an arrival for this tile must not
+          // count for the one before
+          if (kk >= 1) ok = ok && mbar_wait(pv_done, (kk - 1) & 1, a.status);
         }
         // value rows behind the sequence meet P = 0 but may hold anything (NaN): zero
         // them before the P.V product reads them
@@ -375,30 +438,15 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
             *reinterpret_cast<uint4*>(vt + c * C::TK * 128 + (r_lo + i / 8) * 128 + (i % 8) * 16) =
                 make_uint4(0, 0, 0, 0);
           }
+          fence_proxy_async_smem();   // the zeroed rows are read by the tensor core
         }
-        // O *= alpha before this tile's P.V, once the previous one has completed
-        if (k >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          ok = ok && mbar_wait(pv_done + 8 * ((kk - 1) & 1), ((kk - 1) >> 1) & 1, a.status);
-          tc::fence_after();
-#pragma unroll
-          for (int q4 = 0; q4 < C::D_H / 16; ++q4) {
-            float o[16];
-            tc::ld16(trow + C::O_COL + q4 * 16, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= alpha;
-            tc::st16(trow + C::O_COL + q4 * 16, o);
-          }
-          tc::wait_st();
-        }
-        fence_proxy_async_smem();   // P and the zeroed rows are read by the tensor core
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * pb);
+        if (lane == 0) mbar_arrive(p_full);
       }
       {   // the last P.V of the piece (and with it every MMA before) has completed
         const int kl = kt + nk - 1;
-        ok = ok && mbar_wait(pv_done + 8 * (kl & 1), (kl >> 1) & 1, a.status);
+        ok = ok && mbar_wait(pv_done, kl & 1, a.status);
         tc::fence_after();
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -419,7 +467,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
               for (int i = 0; i < 4; ++i)
                 dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             } else if (a.out_bf16) {
-              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * C::D_H + q4 * 16);
+              uint4* dst =
+                  reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * C::D_H + q4 * 16);
 #pragma unroll
               for (int i = 0; i < 2; ++i)
                 dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
@@ -439,28 +488,14 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           else if (a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
         }
       }
+      kt += nk;
       tc::fence_before();   // O has been read: the next piece's MMAs may overwrite it
+      __syncthreads();
+      tc::fence_after();
     }
-    kt += nk;
-    if (threadIdx.x == 0) {
-      if (p.k0 == 0 && nk < p.nt)   // started here, ended elsewhere: where its pieces are
-        a.meta[blockIdx.x] = make_int4(ts.cta_of(walk.u + p.nt - 1) - (int)blockIdx.x + 1, p.b, p.g, p.rb);
-      more = walk.next();
-      piece = walk.p;
-    }
-    __syncthreads();   // all roles are done with the piece; the next one's is in place
-    tc::fence_after();
   }
 
-  // ---- nothing in flight may outlive the CTA: copies, then MMAs; free the memory
-  if (warp == 0 && lane == 0) {
-    for (int kk = max(0, issued - C::STAGES); kk < issued; ++kk)
-      mbar_wait(full + 8 * (kk % C::STAGES), (kk / C::STAGES) & 1, a.status);
-  }
-  if (warp == 1 && lane == 0) {
-    tc::commit(fin);
-    mbar_wait(fin, 0, a.status);
-  }
+  // ---- every role is done with the tensor memory: free it
   tc::fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -521,6 +556,19 @@ cudaError_t launch_paged_tc(const gva_shape_t& sh, const PagedArgs& a, const CUt
     using C = decltype(c);
     const size_t smem = C::SMEM;
     if ((err = ensure_max_smem(paged_tc_kernel<C>, smem)) != cudaSuccess) return;
+    if constexpr (C::SPLIT_REGS) {
+      // the register split needs the full 128 at launch (it would wait forever on fewer)
+      static std::atomic<bool> checked{false};
+      if (!checked.load(std::memory_order_relaxed)) {
+        cudaFuncAttributes fa;
+        if ((err = cudaFuncGetAttributes(&fa, paged_tc_kernel<C>)) != cudaSuccess) return;
+        if (fa.numRegs <= 120) {
+          err = cudaErrorInvalidConfiguration;
+          return;
+        }
+        checked.store(true, std::memory_order_relaxed);
+      }
+    }
     err = launch_pdl(paged_tc_kernel<C>, dim3(a.grid), dim3(C::THREADS), smem, st, a, tv, tk);
   });
   return err;
