@@ -58,22 +58,56 @@ __device__ __forceinline__ int slot_of(const PagedArgs& a, const int* row, int t
 // gets the same number of tiles whatever the lengths, and a block whose units fall
 // to several CTAs is merged from their pieces.
 // ---------------------------------------------------------------------------
+// Sum over i in [0, n) of floor((a i + b) / m), all >= 0 (the Euclidean recursion on
+// the lattice points under a line).
+__device__ inline unsigned long long floor_sum(unsigned long long n, unsigned long long m,
+                                               unsigned long long a, unsigned long long b) {
+  unsigned long long sum = 0;
+  for (;;) {
+    if (a >= m) {
+      sum += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const unsigned long long y = a * n + b;
+    if (y < m) return sum;
+    n = y / m;
+    b = y % m;
+    const unsigned long long t = m;
+    m = a;
+    a = t;
+  }
+}
+
 template <int M, int TK>
 struct RowBlocks {
   const PagedArgs& a;
-  __device__ __forceinline__ int blocks(const SeqRows& s) const { return (s.n * a.hpr + M - 1) / M; }
+  __device__ __forceinline__ int blocks(const SeqRows& s) const {
+    return (int)((unsigned)(s.n * a.hpr + M - 1) / M);
+  }
   __device__ __forceinline__ int kv_end(const SeqRows& s, int rb) const {
-    const int last = min(s.n - 1, ((rb + 1) * M - 1) / a.hpr);
+    const int last = min(s.n - 1, (int)((unsigned)((rb + 1) * M - 1) / (unsigned)a.hpr));
     return max(0, s.L - s.n + last + 1);
   }
   __device__ __forceinline__ int tiles(const SeqRows& s, int rb) const {
-    return max(1, (kv_end(s, rb) + TK - 1) / TK);
+    return max(1, (int)((unsigned)(kv_end(s, rb) + TK - 1) / TK));
   }
   __device__ long long units(int b) const {
     const SeqRows s = seq_rows(a, b);
-    long long u = 0;
     const int nb = blocks(s);
-    for (int rb = 0; rb < nb; ++rb) u += tiles(s, rb);
+    if (nb == 0) return 0;
+    long long u = tiles(s, nb - 1);
+    if (nb <= 8 || s.L < s.n) {
+      for (int rb = 0; rb < nb - 1; ++rb) u += tiles(s, rb);
+    } else {
+      // full blocks: ceil((L - n + floor(((rb + 1) M - 1) / hpr) + 1) / TK), one floor
+      // of a line in rb
+      const unsigned long long h = a.hpr;
+      u += (long long)floor_sum(nb - 1, h * TK, M, M - 1 + h * (unsigned long long)(s.L - s.n + TK));
+    }
     return u * a.G;
   }
 };
@@ -83,7 +117,8 @@ struct RowPiece {
   int b, g, rb, k0, k1, nt;
 };
 
-// The pieces of a CTA's units [u, end), in order (one thread walks).
+// The pieces of a CTA's units [u, end), in order.  first() is called by whole warps,
+// next() by any thread that called first().
 template <int M, int TK>
 struct RowWalk {
   RowBlocks<M, TK> rb;
@@ -96,20 +131,34 @@ struct RowWalk {
     if (u >= end) return false;
     p.b = seq_at(prefix, rb.a.B, u);
     s = seq_rows(rb.a, p.b);
+    // the block that holds unit u: lanes take consecutive blocks
     int rem = u - prefix[p.b];
-    p.rb = 0;
-    for (;;) {
-      p.nt = rb.tiles(s, p.rb);
-      if (rem < rb.a.G * p.nt) break;
-      rem -= rb.a.G * p.nt;
-      ++p.rb;
+    const int nb = rb.blocks(s), lane = threadIdx.x & 31;
+    for (int base = 0;; base += 32) {
+      const int i = base + lane;
+      const int mine = i < nb ? rb.a.G * rb.tiles(s, i) : 0;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned over = __ballot_sync(0xffffffffu, incl > rem);
+      if (over || base + 32 >= nb) {
+        const int l = over ? __ffs(over) - 1 : 31;
+        rem -= __shfl_sync(0xffffffffu, incl - mine, l);
+        p.rb = base + l;
+        break;
+      }
+      rem -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    p.g = rem / p.nt;
+    p.nt = rb.tiles(s, p.rb);
+    p.g = (unsigned)rem / (unsigned)p.nt;
     p.k0 = rem - p.g * p.nt;
     clip();
     return true;
   }
-  __device__ void clip() { p.k1 = min(p.nt, p.k0 + (end - u)); }
+  __device__ __forceinline__ void clip() { p.k1 = min(p.nt, p.k0 + (end - u)); }
   __device__ bool next() {
     u += p.k1 - p.k0;
     if (u >= end) return false;

@@ -85,7 +85,7 @@ cudaError_t launch_paged_mma(const gva_shape_t& sh, const PagedArgs& a, int cols
 
 bool paged_tc_supported(const gva_shape_t& sh, int page);
 int paged_tc_tile(const gva_shape_t& sh);
-int paged_tc_grid(const gva_shape_t& sh, int n_rows, int num_sms, long long max_total);
+int paged_tc_grid(const gva_shape_t& sh, int n_rows, int max_new, int num_sms, long long max_total);
 cudaError_t launch_paged_tc(const gva_shape_t& sh, const PagedArgs& a, const CUtensorMap& tv,
                             const CUtensorMap& tk, cudaStream_t st);
 

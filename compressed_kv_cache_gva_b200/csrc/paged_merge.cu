@@ -149,7 +149,8 @@ cudaError_t launch_paged_merge_seq(const PagedArgs& a, int tile, cudaStream_t st
 }
 
 cudaError_t launch_paged_merge_rows(const PagedArgs& a, int M, cudaStream_t st) {
-  const dim3 grid(a.grid, M / 8);
+  const long long most = (long long)a.max_new * a.hpr;   // rows of the fullest block
+  const dim3 grid(a.grid, (unsigned)(((most < M ? most : M) + 7) / 8));
   if (M == kPagedTcRows) return launch_pdl(paged_merge_rows_kernel<kPagedTcRows>, grid, dim3(256), 0, st, a);
   return launch_pdl(paged_merge_rows_kernel<kPagedSimtRows>, grid, dim3(256), 0, st, a);
 }

@@ -65,9 +65,12 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
   const TileSplit ts = make_split(prefix[a.B], (int)gridDim.x, 0);
   if (tid == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   RowWalk<kM, kTK> walk{blocks, prefix, ts.first(blockIdx.x), ts.first(blockIdx.x + 1), {}, {}};
-  if (tid == 0) {
-    more = walk.first();
-    piece = walk.p;
+  if (tid < 32) {
+    const bool any = walk.first();
+    if (tid == 0) {
+      more = any;
+      piece = walk.p;
+    }
   }
   __syncthreads();
   while (more) {

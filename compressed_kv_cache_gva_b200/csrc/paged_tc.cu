@@ -32,9 +32,14 @@ namespace gva {
 
 namespace {
 
-template <int D_H_, int DRP_, bool HILO_>
+template <int D_H_, int DRP_, bool HILO_, int MS_>
 struct PtCfg {
   static constexpr int D_H = D_H_, DRP = DRP_;
+  // Query rows kept in shared memory.  Where no block has more than 32 rows (drafts)
+  // only those are stored; the MMA's other rows read whatever lies behind them, which
+  // no one looks at, and the ring gets the memory: with 3 instead of 2 stages a draft
+  // step no longer waits a DRAM latency per tile.
+  static constexpr int MS = MS_;
   static constexpr bool HILO = HILO_;        // P in two bf16 halves (float32 output)
   static constexpr int M = kPagedTcRows;
   // Keys per tile.  S, P and O of two CTAs share the SM's 512 tensor-memory columns:
@@ -42,8 +47,8 @@ struct PtCfg {
   // has two halves.  Longer tiles have fewer hand-offs per key.
   static constexpr int TK = D_H == 64 && !HILO ? 128 : 64;
   static constexpr int CB = D_H / 64, KS = D_H / 16, RS = DRP / 16;
-  static constexpr int QB = M * D_H * 2;     // q~ hi (or lo): CB blocks of M rows x 128 B
-  static constexpr int QRB = DRP ? (M * DRP * 2 + 1023) / 1024 * 1024 : 0;
+  static constexpr int QB = MS * D_H * 2;    // q~ hi (or lo): CB blocks of MS rows x 128 B
+  static constexpr int QRB = DRP ? (MS * DRP * 2 + 1023) / 1024 * 1024 : 0;
   static constexpr int VB = CB * TK * 128;
   static constexpr int KRB = DRP * TK * 2;
   static constexpr int STAGE = VB + (KRB + 1023) / 1024 * 1024;
@@ -55,11 +60,13 @@ struct PtCfg {
   static constexpr int STAGES = STAGES_RAW > 6 ? 6 : STAGES_RAW;
   static constexpr int PER_SM = TWO ? 2 : 1;
   static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
-  // full[S], empty[S], s_full, s_free, p_full, pv_done, fin
-  static constexpr int NBAR = 2 * STAGES + 5;
-  // the unit prefix of the prologue lies where the ring is later
+  // full[S], empty[S], s_full, s_free, p_full, pv_done, q_full, q_free, fin
+  static constexpr int NBAR = 2 * STAGES + 7;
+  // the unit prefix of the prologue lies where the queries and the ring are later
   static constexpr int SMEM = 1024 + OFF_BAR + NBAR * 8 + 8;
-  static_assert(STAGES * STAGE >= (int)sizeof(int) * (kMaxBatch + 1) + 16 + 33 * 8, "unit prefix");
+  static_assert(OFF_BAR >= (int)sizeof(int) * (2 * kMaxBatch + 1) + 16 + 33 * 8, "unit prefix");
+  // rows past MS are read up to a full block's size behind each operand
+  static_assert(SMEM - 1024 >= 2 * QB + 2 * QRB + M * 128, "operand reads stay inside");
   static_assert(STAGES >= 2 && SMEM <= 227 * 1024, "shared memory");
   static constexpr uint32_t S_COL = 0, P_COL = TK, P_COLS = TK / 2;
   static constexpr uint32_t O_COL = D_H == 64 && !HILO ? 192 : 128;
@@ -70,7 +77,7 @@ struct PtCfg {
   static constexpr uint32_t SW_R = DRP == 32 ? tc::kSw64 : tc::kSw32;
   static constexpr uint32_t SBO_R = DRP * 2 * 8;
   // A row of 128 scores does not fit the 128 registers that two CTAs leave a thread:
-  // the softmax warps take theirs from the other four (72 + 184 = 2 x 128)
+  // the softmax warps take theirs from the other four (88 + 168 = 2 x 128)
   static constexpr bool SPLIT_REGS = TK == 128 && PER_SM == 2;
 };
 
@@ -111,45 +118,50 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Queries of a piece -> shared memory: bf16 hi and lo halves, swizzled K-major rows.
+// Queries of a piece -> shared memory: bf16 hi and lo halves, swizzled K-major rows;
+// by threads tid, tid + nthr, ...  Four 32-byte loads are in flight per thread.
 template <class C>
 __device__ __forceinline__ void load_queries(const PagedArgs& a, const RowPiece& p, const SeqRows& s,
-                                             uint8_t* sm) {
-  const int hpr = a.hpr, dq = C::D_H + a.d_r, row0 = p.rb * C::M, rows = min(C::M, s.n * hpr - row0);
-#pragma unroll 2
-  for (int e = threadIdx.x; e < C::M * (C::D_H / 8); e += C::THREADS) {
-    const int r = e / (C::D_H / 8), c = e % (C::D_H / 8);
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (r < rows) {
-      const int R = row0 + r;
-      const float* src = a.q_abs + ((long long)(s.r0 + R / hpr) * a.H + p.g * hpr + R % hpr) * dq + c * 8;
-      const float4 u = *reinterpret_cast<const float4*>(src);
-      const float4 v = *reinterpret_cast<const float4*>(src + 4);
-      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-      x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-    }
-    uint4 lo;
-    const uint4 hi = split_bf16(x, lo);
-    const uint32_t o = (c / 8) * (C::M * 128) + sw128(r, c % 8);
-    *reinterpret_cast<uint4*>(sm + o) = hi;
-    *reinterpret_cast<uint4*>(sm + o + C::QB) = lo;
-  }
-  if constexpr (C::DRP > 0) {
-    for (int e = threadIdx.x; e < C::M * (C::DRP / 8); e += C::THREADS) {
-      const int r = e / (C::DRP / 8), c = e % (C::DRP / 8), R = row0 + r;
-      const float* src = a.q_abs + ((long long)(s.r0 + R / hpr) * a.H + p.g * hpr + R % hpr) * dq + C::D_H;
-      float x[8];
+                                             uint8_t* sm, int tid, int nthr) {
+  constexpr int CH = (C::D_H + C::DRP) / 8, NC = C::MS * CH;   // 8-element chunks
+  const int hpr = a.hpr, dq = C::D_H + a.d_r, row0 = p.rb * C::M, rows = min(C::MS, s.n * hpr - row0);
+  for (int e0 = tid; e0 < NC; e0 += 4 * nthr) {
+    float4 x[4][2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = (r < rows && c * 8 + i < a.d_r) ? src[c * 8 + i] : 0.f;
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + u * nthr, r = e / CH, c = e % CH;
+      x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e < NC && r < rows && c * 8 < dq) {
+        const unsigned R = row0 + r, qi = R / (unsigned)hpr;
+        const float* src = a.q_abs + ((long long)(s.r0 + (int)qi) * a.H + p.g * hpr + (int)(R - qi * hpr)) * dq + c * 8;
+        x[u][0] = *reinterpret_cast<const float4*>(src);
+        x[u][1] = *reinterpret_cast<const float4*>(src + 4);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + u * nthr, r = e / CH, c = e % CH;
+      if (e >= NC) break;
+      const float y[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
       uint4 lo;
-      const uint4 hi = split_bf16(x, lo);
-      const uint32_t o = C::OFF_QR + sw_pos<C::DRP>(r, c);
+      const uint4 hi = split_bf16(y, lo);
+      const bool pos = c >= C::D_H / 8;
+      const uint32_t o = pos ? C::OFF_QR + sw_pos<C::DRP>(r, c - C::D_H / 8)
+                             : (c / 8) * (C::MS * 128) + sw128(r, c % 8);
       *reinterpret_cast<uint4*>(sm + o) = hi;
-      *reinterpret_cast<uint4*>(sm + o + C::QRB) = lo;
+      *reinterpret_cast<uint4*>(sm + o + (pos ? C::QRB : C::QB)) = lo;
     }
   }
   fence_proxy_async_smem();   // the queries are read by the tensor core (async proxy)
 }
+
+// A softmax warp's place in the walk over the CTA's pieces.
+struct SoftmaxPiece {
+  RowPiece p;
+  SeqRows s;
+  int u, end;
+  bool more;
+};
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
@@ -161,13 +173,13 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   const uint32_t full = smem_u32(bars), empty = full + 8 * C::STAGES;
   const uint32_t s_full = empty + 8 * C::STAGES, s_free = s_full + 8;
-  const uint32_t p_full = s_free + 8, pv_done = p_full + 8, fin = pv_done + 8;
+  const uint32_t p_full = s_free + 8, pv_done = p_full + 8, q_full = pv_done + 8;
+  const uint32_t q_free = q_full + 8, fin = q_free + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
-  int* prefix = reinterpret_cast<int*>(sm + C::OFF_RING);
+  int* prefix = reinterpret_cast<int*>(sm);
   long long* wtmp = reinterpret_cast<long long*>(
-      (reinterpret_cast<uintptr_t>(prefix + a.B + 1) + 15) & ~uintptr_t(15));
-  __shared__ RowPiece piece;
-  __shared__ int more;
+      (reinterpret_cast<uintptr_t>(prefix + 2 * a.B + 1) + 15) & ~uintptr_t(15));
+  int* units = prefix + a.B + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hpr = a.hpr;
   if (threadIdx.x == 0) {
@@ -179,6 +191,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     mbar_init(s_free, 4);
     mbar_init(p_full, 4);
     mbar_init(pv_done, 1);
+    mbar_init(q_full, 2);
+    mbar_init(q_free, 1);
     mbar_init(fin, 1);
     fence_barrier_init();
   }
@@ -195,45 +209,46 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   pdl_trigger();   // the merge waits for this kernel before it reads
   if (blockIdx.x == 0 && a.flag_errors) flag_bad_sequences(a);
   const RowBlocks<C::M, C::TK> blocks{a};
-  if (block_scan(a.B, [&](int b) { return blocks.units(b); }, prefix, wtmp) >= (1ll << 31) &&
-      threadIdx.x == 0)
-    atomicOr(a.status, GVA_DEVERR_RANGE);
-  const TileSplit ts = make_split(prefix[a.B], (int)gridDim.x, 0);
-  RowWalk<C::M, C::TK> walk{blocks, prefix, ts.first(blockIdx.x), ts.first(blockIdx.x + 1), {}, {}};
-  if (threadIdx.x == 0) {
-    a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    more = walk.first();
-    piece = walk.p;
+  {
+    const int per = (a.B + C::THREADS - 1) / C::THREADS;   // as block_scan deals them out
+    for (int b = threadIdx.x * per; b < min((int)(threadIdx.x + 1) * per, a.B); ++b)
+      units[b] = (int)min(blocks.units(b), 0x7fffffffll);
+    if (block_scan(a.B, [&](int b) { return (long long)units[b]; }, prefix, wtmp) >= (1ll << 31) &&
+        threadIdx.x == 0)
+      atomicOr(a.status, GVA_DEVERR_RANGE);
   }
+  const TileSplit ts = make_split(prefix[a.B], (int)gridDim.x, 0);
+  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+  // Every role walks the CTA's pieces by itself.
+  RowWalk<C::M, C::TK> walk{blocks, prefix, ts.first(blockIdx.x), ts.first(blockIdx.x + 1), {}, {}};
+  bool more = walk.first();
+  fence_proxy_async_smem();   // the prefix was read where TMA writes the ring
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
+  const RowPiece& p = walk.p;
+  const SeqRows& s = walk.s;
 
   // kt: tiles of this CTA before the piece; all barrier phases count from it.
   // ok: false once a bounded wait gave up: skip work, keep the order.
-  // Both halves of the CTA walk the same pieces: load the queries, barrier, their
-  // roles, barrier.
   int kt = 0;
   bool ok = true;
   if (warp < 4) {
-    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    int issued = 0;
-    while (more) {
-      const RowPiece p = piece;
-      const SeqRows s = seq_rows(a, p.b);
-      const int nk = p.k1 - p.k0;
-      load_queries<C>(a, p, s, sm);
-      __syncthreads();
-      if (warp == 0) {
-        // -------------------------------------------------------- producer
-        const int per_tile = C::TK >> a.box_log2;
+    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      int issued = 0;
+      const int per_tile = C::TK >> a.box_log2;
+      for (; more; more = walk.next()) {
+        const int nk = p.k1 - p.k0, end = p.k1 * per_tile;
+        if (lane == 0 && p.k0 == 0 && nk < p.nt)   // started here, ended elsewhere: where its pieces are
+          a.meta[blockIdx.x] = make_int4(ts.cta_of(walk.u + p.nt - 1) - (int)blockIdx.x + 1, p.b, p.g, p.rb);
         const int* row = a.table + (long long)p.b * a.table_stride;
         int base = p.k0 * per_tile;
-        const int end = p.k1 * per_tile;
         auto look = [&](int i) { return i < end ? slot_of(a, row, i << a.box_log2, s.L) : a.num_slots; };
         int y_now = look(base + lane), y_next = look(base + 32 + lane);
-        for (int k = 0; k < nk; ++k) {
+        for (int k = 0; k < nk && ok; ++k) {
           const int box0 = (p.k0 + k) * per_tile;
           if (box0 - base >= 32) {
             base += 32;
@@ -241,7 +256,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
             y_next = look(base + 32 + lane);
           }
           const int kk = kt + k, sg = kk % C::STAGES;
-          if (ok && kk >= C::STAGES) ok = mbar_wait(empty + 8 * sg, ((kk / C::STAGES) - 1) & 1, a.status);
+          if (kk >= C::STAGES) ok = mbar_wait(empty + 8 * sg, ((kk / C::STAGES) - 1) & 1, a.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint32_t fb = full + 8 * sg, st = sb + C::OFF_RING + sg * C::STAGE;
@@ -259,97 +274,110 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           }
           issued = kk + 1;
         }
-      } else if (warp == 1 && lane == 0) {
-        // -------------------------------------------------------- MMA issue
-        constexpr uint32_t idS = tc::idesc_bf16(C::M, C::TK, 0, 0);   // Q (K-major) x V^T (K-major)
-        constexpr uint32_t idO = tc::idesc_bf16(C::M, C::D_H, 0, 1);  // P (tensor memory) x V (MN-major)
-        for (int k = 0; k <= nk; ++k) {
-          if (k < nk) {
-            const int kk = kt + k, sg = kk % C::STAGES;
-            ok = ok && mbar_wait(full + 8 * sg, (kk / C::STAGES) & 1, a.status);
-            if (kk >= 1) ok = ok && mbar_wait(s_free, (kk - 1) & 1, a.status);
-            tc::fence_after();
-            if (ok) {
-              const uint32_t d = tmem + C::S_COL, vt = sb + C::OFF_RING + sg * C::STAGE;
-#pragma unroll
-              for (int ks = 0; ks < C::KS; ++ks) {
-                const uint32_t kb = (ks >> 2) * (C::M * 128) + (ks & 3) * 32;
-                const uint64_t bq =
-                    tc::smem_desc(vt + (ks >> 2) * (C::TK * 128) + (ks & 3) * 32, 16, 1024, tc::kSw128);
-                tc::mma_bf16(d, tc::smem_desc(sb + kb, 16, 1024, tc::kSw128), bq, idS, ks > 0);
-                tc::mma_bf16(d, tc::smem_desc(sb + C::QB + kb, 16, 1024, tc::kSw128), bq, idS, 1);
-              }
-#pragma unroll
-              for (int rs = 0; rs < C::RS; ++rs) {
-                const uint64_t bk = tc::smem_desc(vt + C::VB + rs * 32, 16, C::SBO_R, C::SW_R);
-                tc::mma_bf16(d, tc::smem_desc(sb + C::OFF_QR + rs * 32, 16, C::SBO_R, C::SW_R), bk, idS, 1);
-                tc::mma_bf16(d, tc::smem_desc(sb + C::OFF_QR + C::QRB + rs * 32, 16, C::SBO_R, C::SW_R), bk,
-                             idS, 1);
-              }
-            }
-            tc::commit(s_full);
-          }
-          if (k >= 1) {   // P.V of the tile before
-            const int kp = kt + k - 1, sp = kp % C::STAGES;
-            ok = ok && mbar_wait(p_full, kp & 1, a.status);
-            tc::fence_after();
-            if (ok) {
-              const uint32_t vt = sb + C::OFF_RING + sp * C::STAGE;
-#pragma unroll
-              for (int h = 0; h < (C::HILO ? 2 : 1); ++h)
-#pragma unroll
-                for (int kk = 0; kk < C::TK / 16; ++kk)
-                  tc::mma_bf16_ts(tmem + C::O_COL, tmem + C::P_COL + h * C::P_COLS + kk * 8,
-                                  tc::smem_desc(vt + kk * 16 * 128, C::TK * 128, 1024, tc::kSw128), idO,
-                                  (k > 1 || h > 0 || kk > 0) ? 1u : 0u);
-            }
-            tc::commit(pv_done);
-            tc::commit(empty + 8 * sp);
-          }
-        }
+        kt += nk;
       }
-      __syncwarp();   // the issuing lanes rejoin their warps before the barrier
-      kt += nk;
-      if (threadIdx.x == 0) {
-        if (p.k0 == 0 && nk < p.nt)   // started here, ended elsewhere: where its pieces are
-          a.meta[blockIdx.x] = make_int4(ts.cta_of(walk.u + p.nt - 1) - (int)blockIdx.x + 1, p.b, p.g, p.rb);
-        more = walk.next();
-        piece = walk.p;
-      }
-      __syncwarp();
-      __syncthreads();   // all roles are done with the piece; the next one's is in place
-      tc::fence_after();
-    }
-    // ---- nothing in flight may outlive the CTA: copies, then MMAs
-    if (warp == 0 && lane == 0) {
+      // no copy in flight may outlive the CTA
       for (int kk = max(0, issued - C::STAGES); kk < issued; ++kk)
         mbar_wait(full + 8 * (kk % C::STAGES), (kk / C::STAGES) & 1, a.status);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issue
+      if (lane == 0) {
+        constexpr uint32_t idS = tc::idesc_bf16(C::M, C::TK, 0, 0);   // Q (K-major) x V^T (K-major)
+        constexpr uint32_t idO = tc::idesc_bf16(C::M, C::D_H, 0, 1);  // P (tensor memory) x V (MN-major)
+        for (int i = 0; more; more = walk.next(), ++i) {
+          const int nk = p.k1 - p.k0;
+          ok = ok && mbar_wait(q_full, i & 1, a.status);
+          for (int k = 0; k <= nk; ++k) {
+            if (k < nk) {
+              const int kk = kt + k, sg = kk % C::STAGES;
+              ok = ok && mbar_wait(full + 8 * sg, (kk / C::STAGES) & 1, a.status);
+              if (kk >= 1) ok = ok && mbar_wait(s_free, (kk - 1) & 1, a.status);
+              tc::fence_after();
+              if (ok) {
+                const uint32_t d = tmem + C::S_COL, vt = sb + C::OFF_RING + sg * C::STAGE;
+#pragma unroll
+                for (int ks = 0; ks < C::KS; ++ks) {
+                  const uint32_t kb = (ks >> 2) * (C::MS * 128) + (ks & 3) * 32;
+                  const uint64_t bq =
+                      tc::smem_desc(vt + (ks >> 2) * (C::TK * 128) + (ks & 3) * 32, 16, 1024, tc::kSw128);
+                  tc::mma_bf16(d, tc::smem_desc(sb + kb, 16, 1024, tc::kSw128), bq, idS, ks > 0);
+                  tc::mma_bf16(d, tc::smem_desc(sb + C::QB + kb, 16, 1024, tc::kSw128), bq, idS, 1);
+                }
+#pragma unroll
+                for (int rs = 0; rs < C::RS; ++rs) {
+                  const uint64_t bk = tc::smem_desc(vt + C::VB + rs * 32, 16, C::SBO_R, C::SW_R);
+                  tc::mma_bf16(d, tc::smem_desc(sb + C::OFF_QR + rs * 32, 16, C::SBO_R, C::SW_R), bk, idS, 1);
+                  tc::mma_bf16(d, tc::smem_desc(sb + C::OFF_QR + C::QRB + rs * 32, 16, C::SBO_R, C::SW_R), bk,
+                               idS, 1);
+                }
+              }
+              tc::commit(s_full);
+              if (k == nk - 1) tc::commit(q_free);   // the piece's queries have been read
+            }
+            if (k >= 1) {   // P.V of the tile before
+              const int kp = kt + k - 1, sp = kp % C::STAGES;
+              ok = ok && mbar_wait(p_full, kp & 1, a.status);
+              tc::fence_after();
+              if (ok) {
+                const uint32_t vt = sb + C::OFF_RING + sp * C::STAGE;
+#pragma unroll
+                for (int h = 0; h < (C::HILO ? 2 : 1); ++h)
+#pragma unroll
+                  for (int kk = 0; kk < C::TK / 16; ++kk)
+                    tc::mma_bf16_ts(tmem + C::O_COL, tmem + C::P_COL + h * C::P_COLS + kk * 8,
+                                    tc::smem_desc(vt + kk * 16 * 128, C::TK * 128, 1024, tc::kSw128), idO,
+                                    (k > 1 || h > 0 || kk > 0) ? 1u : 0u);
+              }
+              tc::commit(pv_done);
+              tc::commit(empty + 8 * sp);
+            }
+          }
+          kt += nk;
+        }
+        // every MMA has completed before the tensor memory is freed
+        tc::commit(fin);
+        mbar_wait(fin, 0, a.status);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- queries of the next piece
+      for (int i = 0; more; more = walk.next(), ++i) {
+        if (i > 0) {
+          ok = ok && mbar_wait(q_free, (i - 1) & 1, a.status);
+          load_queries<C>(a, p, s, sm, threadIdx.x - 64, 64);
+        } else {   // nothing else to do yet: the softmax warps help
+          load_queries<C>(a, p, s, sm, threadIdx.x - 64, 192);
+          named_bar_sync(1, 192);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
     }
-    if (warp == 1 && lane == 0) {
-      tc::commit(fin);
-      mbar_wait(fin, 0, a.status);
-    }
-    __syncwarp();
   } else {
-    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int quarter = warp & 3, r = 32 * quarter + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
+    // A row of scores takes most of the registers: the walk waits in shared memory.
+    __shared__ SoftmaxPiece pieces[4];
+    SoftmaxPiece& sp = pieces[quarter];
+    if (more) {
+      load_queries<C>(a, p, s, sm, threadIdx.x - 64, 192);
+      named_bar_sync(1, 192);
+      if (lane == 0) sp = SoftmaxPiece{walk.p, walk.s, walk.u, walk.end};
+    }
+    __syncwarp();
     while (more) {
-      const RowPiece p = piece;
-      const SeqRows s = seq_rows(a, p.b);
-      const int nk = p.k1 - p.k0, row0 = p.rb * C::M, rows = min(C::M, s.n * hpr - row0);
-      load_queries<C>(a, p, s, sm);
-      __syncthreads();
+      const int nk = sp.p.k1 - sp.p.k0, k0 = sp.p.k0, row0 = sp.p.rb * C::M;
+      const int L = sp.s.L, first_lim = sp.s.L - sp.s.n, rows = min(C::M, sp.s.n * hpr - row0);
       // ---------------------------------------------------------- softmax, P, O rescale, output
       // idle: no row of this warp counts.  A row of P meets only its own row of O, so
       // what idle lanes of the tensor memory hold does not matter.
       const bool valid = r < rows, idle = 32 * quarter >= rows;
-      const int R = row0 + r, qi = R / hpr, head = p.g * hpr + R % hpr;
-      const int lim = s.L - s.n + qi;                             // last key of this row
-      const int kv_all = s.L - s.n + row0 / hpr + 1;              // keys every row sees
+            const int lim = first_lim + (row0 + r) / hpr;                // last key of this row
+      const int kv_all = first_lim + row0 / hpr + 1;               // keys every row sees
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < nk; ++k) {
-        const int kk = kt + k, t0 = (p.k0 + k) * C::TK;
+        const int kk = kt + k, t0 = (k0 + k) * C::TK;
         ok = ok && mbar_wait(s_full, kk & 1, a.status);
         tc::fence_after();
         if (!idle) {
@@ -364,7 +392,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           // than the operations themselves
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           if (!ok || t0 + C::TK > kv_all) {   // some row does not see the whole tile
-            const int vis = ok && valid ? min(lim + 1, s.L) - t0 : 0;
+            const int vis = ok && valid ? min(lim + 1, L) - t0 : 0;
 #pragma unroll
             for (int j = 0; j < C::TK; ++j) x[j] = j < vis ? x[j] : -INFINITY;
           }
@@ -383,11 +411,11 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           const float2 neg = make_float2(-ms, -ms);
           float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-          for (int q = 0; q < C::TK / 32; ++q) {   // 32 keys at a time
-            uint32_t hi[16], lo[16];
+          for (int q = 0; q < C::TK / 16; ++q) {   // 16 keys at a time
+            uint32_t hi[8], lo[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float2 e = add2(make_float2(x[32 * q + 2 * i], x[32 * q + 2 * i + 1]), neg);
+            for (int i = 0; i < 8; ++i) {
+              float2 e = add2(make_float2(x[16 * q + 2 * i], x[16 * q + 2 * i + 1]), neg);
               e.x = ex2(e.x);
               e.y = ex2(e.y);
               sum[i & 3] = add2(sum[i & 3], e);
@@ -403,8 +431,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
               ok = ok && mbar_wait(pv_done, (kk - 1) & 1, a.status);
               tc::fence_after();
             }
-            tc::st16u(trow + C::P_COL + q * 16, hi);
-            if constexpr (C::HILO) tc::st16u(trow + C::P_COL + C::P_COLS + q * 16, lo);
+            tc::st8u(trow + C::P_COL + q * 8, hi);
+            if constexpr (C::HILO) tc::st8u(trow + C::P_COL + C::P_COLS + q * 8, lo);
           }
           l = l * alpha + (((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
                            ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y)));
@@ -430,9 +458,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         }
         // value rows behind the sequence meet P = 0 but may hold anything (NaN): zero
         // them before the P.V product reads them
-        if (t0 + C::TK > s.L) {
+        if (t0 + C::TK > L) {
           uint8_t* vt = sm + C::OFF_RING + (kk % C::STAGES) * C::STAGE;
-          const int r_lo = max(s.L - t0, 0), nz = (C::TK - r_lo) * 8;   // 16-byte chunks per block
+          const int r_lo = max(L - t0, 0), nz = (C::TK - r_lo) * 8;   // 16-byte chunks per block
           for (int e = r; e < nz * C::CB; e += 128) {
             const int c = e / nz, i = e % nz;
             *reinterpret_cast<uint4*>(vt + c * C::TK * 128 + (r_lo + i / 8) * 128 + (i % 8) * 16) =
@@ -451,9 +479,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!idle) {
-        const bool whole = nk == p.nt;
-        const long long orow = (long long)(s.r0 + qi) * a.H + head;
-        const long long prt = (long long)piece_slot(p, blockIdx.x) * C::M + r;
+        const bool whole = nk == sp.p.nt;
+        const int R = row0 + r, qi = R / hpr, head = sp.p.g * hpr + R % hpr;
+        const long long orow = (long long)(sp.s.r0 + qi) * a.H + head;
+        const long long prt = (long long)piece_slot(sp.p, blockIdx.x) * C::M + r;
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
         for (int q4 = 0; q4 < C::D_H / 16; ++q4) {
@@ -489,9 +518,17 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         }
       }
       kt += nk;
-      tc::fence_before();   // O has been read: the next piece's MMAs may overwrite it
-      __syncthreads();
-      tc::fence_after();
+      __syncwarp();
+      if (lane == 0) {
+        RowWalk<C::M, C::TK> w{blocks, nullptr, sp.u, sp.end, sp.p, sp.s};
+        sp.more = w.next();
+        sp.p = w.p;
+        sp.s = w.s;
+        sp.u = w.u;
+      }
+      __syncwarp();
+      more = sp.more;
+      tc::fence_before();   // O has been read: the P of the next piece orders its first P.V behind
     }
   }
 
@@ -504,14 +541,15 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   }
 }
 
-// Visit the configuration of (d_h, padded d_r, output type).
+// Visit the configuration of (d_h, padded d_r, output type, rows of a block).
 template <class F>
-bool dispatch(const gva_shape_t& sh, F&& f) {
+bool dispatch(const gva_shape_t& sh, int max_new, F&& f) {
   const int drp = sh.d_r == 0 ? 0 : (sh.d_r <= 16 ? 16 : (sh.d_r <= 32 ? 32 : -1));
-  const bool hilo = sh.out_dtype == GVA_F32;
+  const bool hilo = sh.out_dtype == GVA_F32, few = (long long)max_new * (sh.H / sh.G) <= 32;
 #define GVA_PT(DH, DRP, HILO)                                   \
   if (sh.d_h == DH && drp == DRP && hilo == HILO) {             \
-    f(PtCfg<DH, DRP, HILO>{});                                  \
+    if (few) f(PtCfg<DH, DRP, HILO, 32>{});                     \
+    else f(PtCfg<DH, DRP, HILO, kPagedTcRows>{});               \
     return true;                                                \
   }
 #define GVA_PT_DR(DH, HILO) GVA_PT(DH, 0, HILO) GVA_PT(DH, 16, HILO) GVA_PT(DH, 32, HILO)
@@ -527,18 +565,18 @@ bool dispatch(const gva_shape_t& sh, F&& f) {
 }  // namespace
 
 bool paged_tc_supported(const gva_shape_t& sh, int page) {
-  return sh.cache_dtype == GVA_BF16 && page % 8 == 0 && dispatch(sh, [](auto) {});
+  return sh.cache_dtype == GVA_BF16 && page % 8 == 0 && sh.d_r % 8 == 0 && dispatch(sh, 1, [](auto) {});
 }
 
 int paged_tc_tile(const gva_shape_t& sh) {
   int tk = 0;
-  dispatch(sh, [&](auto c) { tk = decltype(c)::TK; });
+  dispatch(sh, 1, [&](auto c) { tk = decltype(c)::TK; });
   return tk;
 }
 
-int paged_tc_grid(const gva_shape_t& sh, int n_rows, int num_sms, long long max_total) {
+int paged_tc_grid(const gva_shape_t& sh, int n_rows, int max_new, int num_sms, long long max_total) {
   int tk = 64, per_sm = 1;
-  dispatch(sh, [&](auto c) {
+  dispatch(sh, max_new, [&](auto c) {
     tk = decltype(c)::TK;
     per_sm = decltype(c)::PER_SM;
   });
@@ -552,7 +590,7 @@ int paged_tc_grid(const gva_shape_t& sh, int n_rows, int num_sms, long long max_
 cudaError_t launch_paged_tc(const gva_shape_t& sh, const PagedArgs& a, const CUtensorMap& tv,
                             const CUtensorMap& tk, cudaStream_t st) {
   cudaError_t err = cudaErrorNotSupported;
-  dispatch(sh, [&](auto c) {
+  dispatch(sh, a.max_new, [&](auto c) {
     using C = decltype(c);
     const size_t smem = C::SMEM;
     if ((err = ensure_max_smem(paged_tc_kernel<C>, smem)) != cudaSuccess) return;
