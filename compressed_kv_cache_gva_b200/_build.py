@@ -51,10 +51,41 @@ def up_to_date(out: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+# Python binding of the paged serving calls: reads torch tensors directly.
+BIND = os.path.join(PKG, "_bind.so")
+
+
+def build_bind(force: bool = False) -> str:
+    """Compile csrc/bind.cpp against torch's headers and libgva.so."""
+    src = os.path.join(CSRC, "bind.cpp")
+    deps = [src, os.path.abspath(__file__), *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    if not force and os.path.exists(BIND) and all(os.path.getmtime(p) <= os.path.getmtime(BIND) for p in deps):
+        return BIND
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    incs = [*include_paths(), os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+            sysconfig.get_path("include")]
+    tmp = BIND + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[a for i in incs for a in ("-isystem", i)], src, "-o", tmp, "-L" + PKG, "-l:" + os.path.basename(LIB),
+           "-Wl,-rpath,$ORIGIN", "-L" + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the Python binding failed:\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
     """Compile every csrc/*.cu and link them into `out` (default: the package's
     libgva.so).  `extra_flags` go to every nvcc compile (e.g. -DGVA_TRACE)."""
     if not force and up_to_date(out) and (not extra_flags or out != LIB):
+        if out == LIB:
+            build_bind()
         return out
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = _sources()
@@ -79,6 +110,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str =
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, out)
+    if out == LIB:
+        build_bind(force)
     return out
 
 

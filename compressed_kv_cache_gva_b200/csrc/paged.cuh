@@ -26,6 +26,39 @@ __device__ __forceinline__ SeqRows seq_rows(const PagedArgs& a, int b) {
   return s;
 }
 
+// The batch by one warp (B <= 32): lane b holds sequence b and the units before it.
+// No block barrier and no second look at the lengths: a prologue on the critical path
+// of short calls (measured: 2.0 us less per row-block CTA than the block-wide scan).
+constexpr int kLaneBatch = 32;
+struct LaneBatch {
+  SeqRows s;          // this lane's sequence (n = 0 past the batch)
+  int before, units;  // exclusive prefix of the units; this sequence's
+  long long total;
+};
+template <class F>
+__device__ __forceinline__ LaneBatch lane_batch(const PagedArgs& a, F&& units_of) {
+  LaneBatch t;
+  const int lane = threadIdx.x & 31;
+  t.s = SeqRows{0, 0, 0, false};
+  if (lane < a.B) t.s = seq_rows(a, lane);
+  const long long u = t.s.n > 0 ? units_of(t.s) : 0;
+  long long x = u;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += v;
+  }
+  t.total = __shfl_sync(0xffffffffu, x, 31);
+  const bool fits = t.total < (1ll << 31);
+  t.before = fits ? (int)(x - u) : 0;
+  t.units = fits ? (int)u : 0;
+  return t;
+}
+__device__ __forceinline__ SeqRows shfl_rows(const SeqRows& s, int b) {
+  return SeqRows{__shfl_sync(0xffffffffu, s.r0, b), __shfl_sync(0xffffffffu, s.n, b),
+                 __shfl_sync(0xffffffffu, s.L, b), false};
+}
+
 // One CTA reports what is inconsistent in the batch (whole block).
 __device__ inline void flag_bad_sequences(const PagedArgs& a) {
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
@@ -60,23 +93,23 @@ __device__ __forceinline__ int slot_of(const PagedArgs& a, const int* row, int t
 // ---------------------------------------------------------------------------
 // Sum over i in [0, n) of floor((a i + b) / m), all >= 0 (the Euclidean recursion on
 // the lattice points under a line).
-__device__ inline unsigned long long floor_sum(unsigned long long n, unsigned long long m,
-                                               unsigned long long a, unsigned long long b) {
+template <typename U>
+__device__ inline unsigned long long floor_sum(U n, U m, U a, U b) {
   unsigned long long sum = 0;
   for (;;) {
     if (a >= m) {
-      sum += n * (n - 1) / 2 * (a / m);
+      sum += (unsigned long long)n * (n - 1) / 2 * (a / m);
       a %= m;
     }
     if (b >= m) {
-      sum += n * (b / m);
+      sum += (unsigned long long)n * (b / m);
       b %= m;
     }
-    const unsigned long long y = a * n + b;
+    const U y = a * n + b;   // within U where the first a n + b is
     if (y < m) return sum;
     n = y / m;
     b = y % m;
-    const unsigned long long t = m;
+    const U t = m;
     m = a;
     a = t;
   }
@@ -95,21 +128,23 @@ struct RowBlocks {
   __device__ __forceinline__ int tiles(const SeqRows& s, int rb) const {
     return max(1, (int)((unsigned)(kv_end(s, rb) + TK - 1) / TK));
   }
-  __device__ long long units(int b) const {
-    const SeqRows s = seq_rows(a, b);
+  __device__ long long units(const SeqRows& s) const {
     const int nb = blocks(s);
     if (nb == 0) return 0;
     long long u = tiles(s, nb - 1);
-    if (nb <= 8 || s.L < s.n) {
+    if (nb <= 4 || s.L < s.n) {
       for (int rb = 0; rb < nb - 1; ++rb) u += tiles(s, rb);
     } else {
       // full blocks: ceil((L - n + floor(((rb + 1) M - 1) / hpr) + 1) / TK), one floor
       // of a line in rb
-      const unsigned long long h = a.hpr;
-      u += (long long)floor_sum(nb - 1, h * TK, M, M - 1 + h * (unsigned long long)(s.L - s.n + TK));
+      const unsigned long long h = a.hpr, b = M - 1 + h * (unsigned long long)(s.L - s.n + TK);
+      u += b + (unsigned long long)M * nb < (1ull << 32) && h * TK < (1ull << 32)
+               ? (long long)floor_sum<unsigned>(nb - 1, (unsigned)(h * TK), M, (unsigned)b)
+               : (long long)floor_sum<unsigned long long>(nb - 1, h * TK, M, b);
     }
     return u * a.G;
   }
+  __device__ long long units(int b) const { return units(seq_rows(a, b)); }
 };
 
 // A piece: tiles [k0, k1) of block rb of group g of sequence b, which has nt tiles.
@@ -131,8 +166,18 @@ struct RowWalk {
     if (u >= end) return false;
     p.b = seq_at(prefix, rb.a.B, u);
     s = seq_rows(rb.a, p.b);
+    return seek(u - prefix[p.b]);
+  }
+  // the same from one warp's batch
+  __device__ bool first(const LaneBatch& t) {
+    if (u >= end) return false;
+    const unsigned over = __ballot_sync(0xffffffffu, t.before + t.units > u);
+    p.b = __ffs(over) - 1;
+    s = shfl_rows(t.s, p.b);
+    return seek(u - __shfl_sync(0xffffffffu, t.before, p.b));
+  }
+  __device__ bool seek(int rem) {
     // the block that holds unit u: lanes take consecutive blocks
-    int rem = u - prefix[p.b];
     const int nb = rb.blocks(s), lane = threadIdx.x & 31;
     for (int base = 0;; base += 32) {
       const int i = base + lane;

@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   int* tp = reinterpret_cast<int*>(empty + C::STAGES);   // tiles before each sequence
   long long* wtmp =
       reinterpret_cast<long long*>((reinterpret_cast<uintptr_t>(tp + a.B + 1) + 15) & ~uintptr_t(15));
+  __shared__ int4 batch[kLaneBatch];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -125,13 +126,31 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   // queries, lengths, tables and cache rows may come from the kernels before
   pdl_wait();
   pdl_trigger();   // the merge waits for this kernel before it reads
-  // tiles of sequence b: one (masked) tile where it has no key
-  auto tiles = [&](int b) -> long long {
-    const SeqRows s = seq_rows(a, b);
+  // tiles of a sequence: one (masked) tile where it has no key
+  auto tiles = [](const SeqRows& s) -> long long {
     return s.n == 0 ? 0 : max(1, (s.L + C::TT - 1) / C::TT);
   };
-  if (block_scan(a.B, tiles, tp, wtmp) >= (1ll << 31) && threadIdx.x == 0)
-    atomicOr(a.status, GVA_DEVERR_RANGE);
+  long long total;
+  if (a.B <= kLaneBatch) {
+    const LaneBatch t = lane_batch(a, tiles);
+    total = t.total;
+    if (warp == 0) {
+      if (lane < a.B) {
+        tp[lane] = t.before;
+        batch[lane] = make_int4(t.s.r0, t.s.n, t.s.L, 0);
+      }
+      if (lane == 0) tp[a.B] = total < (1ll << 31) ? (int)total : 0;
+    }
+    __syncthreads();
+  } else {
+    total = block_scan(a.B, [&](int b) { return tiles(seq_rows(a, b)); }, tp, wtmp);
+  }
+  auto rows_of = [&](int b) -> SeqRows {
+    if (a.B > kLaneBatch) return seq_rows(a, b);
+    const int4 v = batch[b];
+    return SeqRows{v.x, v.y, v.z, false};
+  };
+  if (total >= (1ll << 31) && threadIdx.x == 0) atomicOr(a.status, GVA_DEVERR_RANGE);
   const TileSplit ts = make_split(tp[a.B], (int)gridDim.x, 0);
   const int T0 = ts.first(blockIdx.x), T1 = ts.first(blockIdx.x + 1);
   if (blockIdx.x == 0) {
@@ -151,7 +170,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     for (int b = b_first; ok && b < a.B && tp[b] < T1; ++b) {
       const int u0 = max(T0, tp[b]) - tp[b], u1 = min(T1, tp[b + 1]) - tp[b];
       if (u1 <= u0) continue;
-      const int L = __ldg(a.seq_len + b);
+      const int L = rows_of(b).L;
       const int* row = a.table + (long long)b * a.table_stride;
       int base = u0 * per_tile;
       const int end = u1 * per_tile;
@@ -204,7 +223,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   for (int b = b_first; b < a.B && tp[b] < T1; ++b) {
     const int u0 = max(T0, tp[b]) - tp[b], u1 = min(T1, tp[b + 1]) - tp[b];
     if (u1 <= u0) continue;
-    const SeqRows sq = seq_rows(a, b);
+    const SeqRows sq = rows_of(b);
     const int ncol = sq.n * a.hpr;
     uint32_t qb[C::NT][C::KS][2], qr[C::NT][C::RS > 0 ? C::RS : 1][2];
     load_query<C>(a, sq, g, ncol, gq, t, qb, qr);

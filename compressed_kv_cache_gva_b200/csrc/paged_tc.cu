@@ -118,41 +118,67 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Queries of a piece -> shared memory: bf16 hi and lo halves, swizzled K-major rows;
-// by threads tid, tid + nthr, ...  Four 32-byte loads are in flight per thread.
-template <class C>
-__device__ __forceinline__ void load_queries(const PagedArgs& a, const RowPiece& p, const SeqRows& s,
-                                             uint8_t* sm, int tid, int nthr) {
-  constexpr int CH = (C::D_H + C::DRP) / 8, NC = C::MS * CH;   // 8-element chunks
-  const int hpr = a.hpr, dq = C::D_H + a.d_r, row0 = p.rb * C::M, rows = min(C::MS, s.n * hpr - row0);
-  for (int e0 = tid; e0 < NC; e0 += 4 * nthr) {
+// Queries of a piece -> shared memory: bf16 hi and lo halves, swizzled K-major rows; by
+// threads tid of nthr.  A thread keeps its chunk of 8 elements and steps over rows, four
+// loads of 32 bytes in flight.
+template <class C, int W>   // W: chunks of the part of a row (content, then positional)
+__device__ __forceinline__ void load_query_part(const PagedArgs& a, const float* base, int rows, int row0,
+                                                uint8_t* dst, int half, bool pos, int width, int tid, int nthr) {
+  const int c = tid % W, step = nthr / W;
+  int r = tid / W;
+  const unsigned R = row0 + r, hpr = a.hpr;
+  unsigned qi = R / hpr, h = R - qi * hpr;
+  const unsigned dqi = step / hpr, dh = step - dqi * hpr;
+  const long long dq = C::D_H + a.d_r, token = (long long)a.H * dq;
+  while (r < C::MS) {
     float4 x[4][2];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int e = e0 + u * nthr, r = e / CH, c = e % CH;
       x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (e < NC && r < rows && c * 8 < dq) {
-        const unsigned R = row0 + r, qi = R / (unsigned)hpr;
-        const float* src = a.q_abs + ((long long)(s.r0 + (int)qi) * a.H + p.g * hpr + (int)(R - qi * hpr)) * dq + c * 8;
+      if (r + u * step < rows && c * 8 < width) {
+        const float* src = base + qi * token + h * dq + c * 8;
         x[u][0] = *reinterpret_cast<const float4*>(src);
         x[u][1] = *reinterpret_cast<const float4*>(src + 4);
       }
+      qi += dqi;
+      h += dh;
+      if (h >= hpr) {
+        h -= hpr;
+        ++qi;
+      }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = e0 + u * nthr, r = e / CH, c = e % CH;
-      if (e >= NC) break;
+    for (int u = 0; u < 4; ++u, r += step) {
+      if (r >= C::MS) break;
       const float y[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
       uint4 lo;
       const uint4 hi = split_bf16(y, lo);
-      const bool pos = c >= C::D_H / 8;
-      const uint32_t o = pos ? C::OFF_QR + sw_pos<C::DRP>(r, c - C::D_H / 8)
-                             : (c / 8) * (C::MS * 128) + sw128(r, c % 8);
-      *reinterpret_cast<uint4*>(sm + o) = hi;
-      *reinterpret_cast<uint4*>(sm + o + (pos ? C::QRB : C::QB)) = lo;
+      const uint32_t o = pos ? sw_pos<C::DRP>(r, c) : (c / 8) * (C::MS * 128) + sw128(r, c % 8);
+      *reinterpret_cast<uint4*>(dst + o) = hi;
+      *reinterpret_cast<uint4*>(dst + o + half) = lo;
     }
   }
+}
+template <class C>
+__device__ __forceinline__ void load_queries(const PagedArgs& a, const RowPiece& p, const SeqRows& s,
+                                             uint8_t* sm, int tid, int nthr) {
+  const int row0 = p.rb * C::M, rows = min(C::MS, s.n * a.hpr - row0), dq = C::D_H + a.d_r;
+  const float* base = a.q_abs + ((long long)s.r0 * a.H + p.g * a.hpr) * dq;
+  load_query_part<C, C::D_H / 8>(a, base, rows, row0, sm, C::QB, false, C::D_H, tid, nthr);
+  if constexpr (C::DRP > 0)
+    load_query_part<C, C::DRP / 8>(a, base + C::D_H, rows, row0, sm + C::OFF_QR, C::QRB, true, a.d_r, tid, nthr);
   fence_proxy_async_smem();   // the queries are read by the tensor core (async proxy)
+}
+// Ask L2 for the queries of a piece that is loaded later.
+template <class C>
+__device__ __forceinline__ void prefetch_queries(const PagedArgs& a, const RowPiece& p, const SeqRows& s, int tid,
+                                                 int nthr) {
+  const int row0 = p.rb * C::M, rows = min(C::MS, s.n * a.hpr - row0), dq = C::D_H + a.d_r;
+  for (int r = tid; r < rows; r += nthr) {
+    const unsigned R = row0 + r, qi = R / (unsigned)a.hpr;
+    const float* src = a.q_abs + ((long long)(s.r0 + (int)qi) * a.H + p.g * a.hpr + (int)(R - qi * a.hpr)) * dq;
+    for (int i = 0; i < dq; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
+  }
 }
 
 // A softmax warp's place in the walk over the CTA's pieces.
@@ -209,19 +235,32 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   pdl_trigger();   // the merge waits for this kernel before it reads
   if (blockIdx.x == 0 && a.flag_errors) flag_bad_sequences(a);
   const RowBlocks<C::M, C::TK> blocks{a};
-  {
+  // Every role walks the CTA's pieces by itself.
+  RowWalk<C::M, C::TK> walk{blocks, prefix, 0, 0, {}, {}};
+  TileSplit ts;
+  long long total;
+  bool more;
+  if (a.B <= kLaneBatch) {
+    const LaneBatch t = lane_batch(a, [&](const SeqRows& s) { return blocks.units(s); });
+    total = t.total;
+    ts = make_split(total < (1ll << 31) ? (int)total : 0, (int)gridDim.x, 0);
+    walk.u = ts.first(blockIdx.x);
+    walk.end = ts.first(blockIdx.x + 1);
+    more = walk.first(t);
+  } else {
     const int per = (a.B + C::THREADS - 1) / C::THREADS;   // as block_scan deals them out
     for (int b = threadIdx.x * per; b < min((int)(threadIdx.x + 1) * per, a.B); ++b)
       units[b] = (int)min(blocks.units(b), 0x7fffffffll);
-    if (block_scan(a.B, [&](int b) { return (long long)units[b]; }, prefix, wtmp) >= (1ll << 31) &&
-        threadIdx.x == 0)
-      atomicOr(a.status, GVA_DEVERR_RANGE);
+    total = block_scan(a.B, [&](int b) { return (long long)units[b]; }, prefix, wtmp);
+    ts = make_split(prefix[a.B], (int)gridDim.x, 0);
+    walk.u = ts.first(blockIdx.x);
+    walk.end = ts.first(blockIdx.x + 1);
+    more = walk.first();
   }
-  const TileSplit ts = make_split(prefix[a.B], (int)gridDim.x, 0);
-  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-  // Every role walks the CTA's pieces by itself.
-  RowWalk<C::M, C::TK> walk{blocks, prefix, ts.first(blockIdx.x), ts.first(blockIdx.x + 1), {}, {}};
-  bool more = walk.first();
+  if (threadIdx.x == 0) {
+    if (total >= (1ll << 31)) atomicOr(a.status, GVA_DEVERR_RANGE);
+    a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
   fence_proxy_async_smem();   // the prefix was read where TMA writes the ring
   tc::fence_before();
   __syncthreads();
@@ -343,6 +382,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       // ---------------------------------------------------------- queries of the next piece
       for (int i = 0; more; more = walk.next(), ++i) {
         if (i > 0) {
+          prefetch_queries<C>(a, p, s, threadIdx.x - 64, 64);
           ok = ok && mbar_wait(q_free, (i - 1) & 1, a.status);
           load_queries<C>(a, p, s, sm, threadIdx.x - 64, 64);
         } else {   // nothing else to do yet: the softmax warps help
@@ -485,29 +525,30 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         const long long prt = (long long)piece_slot(sp.p, blockIdx.x) * C::M + r;
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-        for (int q4 = 0; q4 < C::D_H / 16; ++q4) {
-          float o[16];
-          tc::ld16(trow + C::O_COL + q4 * 16, o);
+        for (int q = 0; q < C::D_H / 64; ++q) {
+          float o[64];
+          tc::ld32(trow + C::O_COL + q * 64, o);
+          tc::ld32(trow + C::O_COL + q * 64 + 32, o + 32);
           tc::wait_ld();
           if (valid && ok) {
             if (!whole) {
-              float4* dst = reinterpret_cast<float4*>(a.part_o + prt * C::D_H + q4 * 16);
+              float4* dst = reinterpret_cast<float4*>(a.part_o + prt * C::D_H + q * 64);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 16; ++i)
                 dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             } else if (a.out_bf16) {
               uint4* dst =
-                  reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * C::D_H + q4 * 16);
+                  reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * C::D_H + q * 64);
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
+              for (int i = 0; i < 8; ++i)
                 dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
                                     pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                                     pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
                                     pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
             } else {
-              float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * C::D_H + q4 * 16);
+              float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * C::D_H + q * 64);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 16; ++i)
                 dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
             }
           }

@@ -9,6 +9,7 @@ the compiled library is missing the first call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -273,30 +274,27 @@ def noalloc_status(stream=None) -> int:
     return int(buf.item())
 
 
-def _arr(t: torch.Tensor, name: str, dtype, shape, dev: int):
-    """Pointer of a contiguous tensor of this type and shape on the current device."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"{name} must live on the current CUDA device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+_bind = None
 
 
-def _rows(t: torch.Tensor, name: str, dtypes, rows: int, cols: int, dev: int):
-    """Pointer of a [rows, >= cols] matrix whose rows may be strided but are dense."""
-    if t.dtype not in dtypes or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols:
-        raise ValueError(f"{name}: expected {dtypes[0]} [{rows}, >= {cols}], got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"{name} must live on the current CUDA device")
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows must be dense and must not overlap")
-    return t.data_ptr()
+def _paged():
+    """The binding of the paged serving calls (csrc/bind.cpp), loaded once; raises if it
+    has not been built."""
+    global _bind
+    if _bind is None:
+        lib()
+        path = os.path.join(_PKG, "_bind.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m compressed_kv_cache_gva_b200._build`")
+        spec = importlib.util.spec_from_file_location("_bind", path)
+        _bind = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_bind)
+    return _bind
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _handle(stream):
+    return None if stream is None else _stream(stream)
 
 
 def plan_pages(page_size: int, num_pages: int, kept_len, n_new, held_in, held_out, free_pages,
@@ -308,20 +306,9 @@ def plan_pages(page_size: int, num_pages: int, kept_len, n_new, held_in, held_ou
     [num_pages]; free_count_in, free_count_out, err_flag [1]; block_table [B, max_pages]
     (rows may be strided); q_start [B + 1]; slot, pos [max_new_tokens].  held_out may be
     held_in, and free_count_out free_count_in."""
-    dev, i32 = torch.cuda.current_device(), torch.int32
-    B, m = kept_len.shape[0], slot.shape[0]
-    table = _rows(block_table, "block_table", (i32,), B, 1, dev)
-    _check(lib().gva_plan_pages(
-        B, int(page_size), int(num_pages), block_table.shape[1], _row_stride(block_table), m,
-        _arr(kept_len, "kept_len", i32, (B,), dev), _arr(n_new, "n_new", i32, (B,), dev),
-        _arr(held_in, "held_in", i32, (B,), dev), _arr(held_out, "held_out", i32, (B,), dev),
-        _arr(free_pages, "free_pages", i32, (num_pages,), dev),
-        _arr(free_count_in, "free_count_in", i32, (1,), dev),
-        _arr(free_count_out, "free_count_out", i32, (1,), dev), table,
-        _arr(q_start, "q_start", i32, (B + 1,), dev), _arr(seq_len, "seq_len", i32, (B,), dev),
-        _arr(n_granted, "n_granted", i32, (B,), dev), _arr(slot, "slot", i32, (m,), dev),
-        _arr(pos, "pos", i32, (m,), dev),
-        None if err_flag is None else _arr(err_flag, "err_flag", i32, (1,), dev), _stream(stream)))
+    _check((_bind or _paged()).plan_pages(
+        page_size, num_pages, kept_len, n_new, held_in, held_out, free_pages, free_count_in, free_count_out,
+        block_table, q_start, seq_len, n_granted, slot, pos, err_flag, _handle(stream)))
 
 
 def paged_workspace_size(shape: Shape, page_size: int, n_rows: int, max_query_len: int,
@@ -339,9 +326,6 @@ def new_paged_workspace(shape: Shape, page_size: int, n_rows: int, max_query_len
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-_TORCH = {F32: torch.float32, BF16: torch.bfloat16}
-
-
 def paged_attention(shape: Shape, page_size: int, q_abs, V_cache, kr_cache, block_table, q_start,
                     seq_len, max_query_len: int, max_total_tokens: int, out, lse=None,
                     workspace=None, stream=None):
@@ -350,21 +334,9 @@ def paged_attention(shape: Shape, page_size: int, q_abs, V_cache, kr_cache, bloc
     q_abs [n_rows, H, d_h + d_r] float32; V_cache [num_slots, G, d_h] and kr_cache
     [num_slots, d_r] (None if d_r == 0); block_table [B, max_pages] int32 (rows may be
     strided); q_start [B + 1] and seq_len [B] int32; out [n_rows, H, d_h]; lse [n_rows, H]."""
-    dev, i32, f32 = torch.cuda.current_device(), torch.int32, torch.float32
-    B, H, G, d_h, d_r = shape.B, shape.H, shape.G, shape.d_h, shape.d_r
-    n, slots, cache = q_abs.shape[0], V_cache.shape[0], _TORCH.get(shape.cache_dtype)
-    if workspace is None or not workspace.is_cuda or workspace.get_device() != dev:
-        raise ValueError("workspace must live on the current CUDA device")
-    _check(lib().gva_paged_attention(
-        ctypes.byref(shape), int(page_size), _arr(q_abs, "q_abs", f32, (n, H, d_h + d_r), dev),
-        _arr(V_cache, "V_cache", cache, (slots, G, d_h), dev),
-        None if d_r == 0 else _arr(kr_cache, "kr_cache", cache, (slots, d_r), dev), slots,
-        _rows(block_table, "block_table", (i32,), B, 1, dev), block_table.shape[1],
-        _row_stride(block_table), _arr(q_start, "q_start", i32, (B + 1,), dev),
-        _arr(seq_len, "seq_len", i32, (B,), dev), n, int(max_query_len), int(max_total_tokens),
-        _arr(out, "out", _TORCH.get(shape.out_dtype), (n, H, d_h), dev),
-        None if lse is None else _arr(lse, "lse", f32, (n, H), dev), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    _check((_bind or _paged()).paged_attention(
+        shape, page_size, q_abs, V_cache, kr_cache, block_table, q_start, seq_len, max_query_len,
+        max_total_tokens, out, lse, workspace, _handle(stream)))
 
 
 def verify_draft(vocab: int, tokens, q_start, target_probs, draft_probs, u_accept, u_sample,
@@ -375,19 +347,9 @@ def verify_draft(vocab: int, tokens, q_start, target_probs, draft_probs, u_accep
     [n_rows, >= vocab] float32 or bfloat16 (rows may be strided; draft_probs None: the
     drafts were not drawn); u_accept [n_rows], u_sample [B] float32; n_accepted, seq_len,
     kept_len [B] int32."""
-    dev, i32, f32 = torch.cuda.current_device(), torch.int32, torch.float32
-    n, B, dt = tokens.shape[0], u_sample.shape[0], target_probs.dtype
-    opt = lambda t, name, k: None if t is None else _arr(t, name, i32, (k,), dev)
-    target = _rows(target_probs, "target_probs", (f32, torch.bfloat16), n, vocab, dev)
-    draft = None if draft_probs is None else _rows(draft_probs, "draft_probs", (dt,), n, vocab, dev)
-    _check(lib().gva_verify_draft(
-        B, int(vocab), n, _arr(tokens, "tokens", i32, (n,), dev),
-        _arr(q_start, "q_start", i32, (B + 1,), dev), dtype_code(dt), target,
-        _row_stride(target_probs), draft, 0 if draft is None else _row_stride(draft_probs),
-        _arr(u_accept, "u_accept", f32, (n,), dev), _arr(u_sample, "u_sample", f32, (B,), dev),
-        _arr(out_tokens, "out_tokens", i32, (n,), dev), _arr(n_accepted, "n_accepted", i32, (B,), dev),
-        opt(seq_len, "seq_len", B), opt(kept_len, "kept_len", B), opt(err_flag, "err_flag", 1),
-        _stream(stream)))
+    _check((_bind or _paged()).verify_draft(
+        vocab, tokens, q_start, target_probs, draft_probs, u_accept, u_sample, out_tokens, n_accepted,
+        seq_len, kept_len, err_flag, _handle(stream)))
 
 
 EXPORTS = ["gva_status_string", "gva_last_error", "gva_absorb_query", "gva_append_cache",
