@@ -7,6 +7,19 @@
 
 namespace gva {
 
+// Order of a call's kernels on the stream.  A kernel waits for the work before it, then
+// lets the next one launch.  The second kernel of a call that has two (`beside`) shares
+// nothing with the first but its inputs: it launched after every CTA of the first had
+// passed its wait, so those are in place, and it runs at the same time.  It waits for
+// the first only before it ends, so that whoever waits for it has waited for both.
+__device__ __forceinline__ void pdl_enter(const PagedArgs& a) {
+  if (!a.beside) pdl_wait();
+  pdl_trigger();
+}
+__device__ __forceinline__ void pdl_leave(const PagedArgs& a) {
+  if (a.beside) pdl_wait();
+}
+
 // Query rows [r0, r0 + n) and cached length of sequence b; n = 0 where the sequence
 // is inconsistent or belongs to the other kernel of the call.
 struct SeqRows {

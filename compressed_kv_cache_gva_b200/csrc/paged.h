@@ -70,6 +70,7 @@ struct PagedArgs {
   int out_bf16;
   int* status;
   int flag_errors;                        // this kernel reports inconsistent sequences
+  int beside;                             // runs beside the kernel before it (see pdl_enter)
   float2* part_ml;
   float* part_o;
   int4* meta;
@@ -96,10 +97,9 @@ cudaError_t launch_paged_simt(const gva_shape_t& sh, const PagedArgs& a, cudaStr
 constexpr int kPagedTcRows = 128;         // query rows (token x head) of a tcgen05 block
 constexpr int kPagedSimtRows = 16;        // of a CUDA-core block
 
-// Merge of the pieces of sequences (mma kernel: one item per sequence) and of row
-// blocks (tcgen05 and CUDA-core kernels: pieces of the item a CTA starts and leaves
-// to its successors).
-cudaError_t launch_paged_merge_seq(const PagedArgs& a, int tile, cudaStream_t st);
-cudaError_t launch_paged_merge_rows(const PagedArgs& a, int rows_per_block, cudaStream_t st);
+// Merge of the pieces of sequences (s: the mma kernel's arguments, with max_new the most
+// new tokens it takes) and of row blocks of M rows (r: the tcgen05 or CUDA-core
+// kernel's), either or both in one launch.
+cudaError_t launch_paged_merge(const PagedArgs* s, const PagedArgs* r, int M, cudaStream_t st);
 
 }  // namespace gva

@@ -196,26 +196,23 @@ gva_status_t paged_attention(const gva_shape_t* shp, int page, const float* q_ab
   ar.grid = p.rows_grid;
   if (p.rows == PagedPlan::kTc && (s = maps(gva::paged_tc_tile(sh), ar, &rv, &rk)) != GVA_OK) return s;
 
-  if (p.rows != PagedPlan::kNone) {
-    const bool tc = p.rows == PagedPlan::kTc;
-    place(ar, p.blk);
-    if ((s = launched(tc ? gva::launch_paged_tc(sh, ar, rv, rk, st) : gva::launch_paged_simt(sh, ar, st),
-                      "paged attention launch")) != GVA_OK)
-      return s;
-    if ((s = launched(gva::launch_paged_merge_rows(ar, tc ? gva::kPagedTcRows : gva::kPagedSimtRows, st),
-                      "paged merge launch")) != GVA_OK)
-      return s;
-  }
+  const bool tc = p.rows == PagedPlan::kTc, rows = p.rows != PagedPlan::kNone;
   if (p.cols) {
     place(am, p.mma);
     if ((s = launched(gva::launch_paged_mma(sh, am, p.cols, mv, mk, st), "paged attention launch")) != GVA_OK)
       return s;
-    gva::PagedArgs mg = am;
-    mg.max_new = p.mma_new;   // heads of a partial: H * mma_new
-    if ((s = launched(gva::launch_paged_merge_seq(mg, gva::paged_mma_tile(sh), st), "paged merge launch")) != GVA_OK)
+  }
+  if (rows) {
+    place(ar, p.blk);
+    ar.beside = p.cols != 0;
+    if ((s = launched(tc ? gva::launch_paged_tc(sh, ar, rv, rk, st) : gva::launch_paged_simt(sh, ar, st),
+                      "paged attention launch")) != GVA_OK)
       return s;
   }
-  return GVA_OK;
+  am.max_new = p.mma_new;   // heads of a partial: H * mma_new
+  return launched(gva::launch_paged_merge(p.cols ? &am : nullptr, rows ? &ar : nullptr,
+                                          tc ? gva::kPagedTcRows : gva::kPagedSimtRows, st),
+                  "paged merge launch");
 }
 
 }  // namespace

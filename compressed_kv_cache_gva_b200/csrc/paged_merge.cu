@@ -16,16 +16,14 @@ __device__ __forceinline__ void store_out(const PagedArgs& a, long long orow, in
   else reinterpret_cast<float*>(a.out)[orow * a.d_h + d] = v;
 }
 
-// Sequences cut by the split-KV kernel.  grid (B, H * rows, d_h / 32), block 32
+// Sequences cut by the split-KV kernel: block (b, h of H * rows, z of d_h / 32), 32
 // columns x PG piece groups: group pg merges pieces pg, pg + PG, ... (all loads
 // requested before the first use), then the groups merge through shared memory.
 constexpr int kPieces = 4;   // pieces per thread in flight
-__global__ void __launch_bounds__(1024) paged_merge_seq_kernel(const PagedArgs a) {
+__device__ __forceinline__ void merge_seq(const PagedArgs& a, int b, int h, int z, int Hp) {
   __shared__ float sm_m[32][33], sm_l[32][33], sm_o[32][33];
-  const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, d = blockIdx.z * 32 + lane;
-  const int pg = threadIdx.x >> 5, npg = blockDim.x >> 5, Hp = gridDim.y, d_h = a.d_h;
-  pdl_trigger();   // successors wait for this kernel before they read its outputs
-  pdl_wait();
+  const int lane = threadIdx.x & 31, d = z * 32 + lane;
+  const int pg = threadIdx.x >> 5, npg = blockDim.x >> 5, d_h = a.d_h;
   const int4 meta = a.meta[b];
   const int n = meta.y;
   if (n <= 1) return;                       // nothing here, or written by its one CTA
@@ -74,21 +72,18 @@ __global__ void __launch_bounds__(1024) paged_merge_seq_kernel(const PagedArgs a
   }
   const long long orow = (long long)(r0 + qi) * a.H + h % a.H;
   if (col) store_out(a, orow, d, L > 0.f ? O / L : 0.f);
-  if (lane == 0 && blockIdx.z == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  if (lane == 0 && z == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
-// Row blocks cut between CTAs.  grid (CTAs of the split, M / 8), block 8 rows x 32
-// lanes: CTA (i, y) merges rows 8 y .. 8 y + 7 of the block that CTA i of the split
-// started and did not end; its pieces lie in slots 2 i + 1, 2 (i + 1), 2 (i + 2), ...
-// A warp holds the piece weights of its row one per lane, then walks the pieces.
-template <int M>
-__global__ void __launch_bounds__(256) paged_merge_rows_kernel(const PagedArgs a) {
-  const int i = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  pdl_trigger();
-  pdl_wait();
+// Row blocks cut between CTAs: a warp per row.  Block (i, y) merges rows y W .. y W + W-1
+// (W warps) of the block that CTA i of the split started and did not end; its pieces lie
+// in slots 2 i + 1, 2 (i + 1), 2 (i + 2), ...  A warp holds the piece weights of its row
+// one per lane, then walks the pieces.
+__device__ __forceinline__ void merge_rows(const PagedArgs& a, int i, int y, int M) {
+  const int r = y * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int4 meta = a.meta[i];
   const int n = meta.x;
-  if (n == 0) return;
+  if (n == 0 || r >= M) return;
   const int b = meta.y, g = meta.z, R = meta.w * M + r;
   const int r0 = a.q_start[b], rows = (a.q_start[b + 1] - r0) * a.hpr;
   if (R >= rows) return;
@@ -136,23 +131,46 @@ __global__ void __launch_bounds__(256) paged_merge_rows_kernel(const PagedArgs a
   if (lane == 0 && a.lse) a.lse[orow] = L > 0.f ? (mx + log2f(L)) * kLn2 : -INFINITY;
 }
 
-}  // namespace
-
-cudaError_t launch_paged_merge_seq(const PagedArgs& a, int tile, cudaStream_t st) {
-  (void)tile;
-  // a sequence has about grid / B + 1 pieces (ragged batches: more for the long ones)
-  const int per_seq = a.grid / a.B + 2;
-  int npg = (per_seq + kPieces - 1) / kPieces;
-  npg = npg < 1 ? 1 : (npg > 32 ? 32 : npg);
-  const dim3 grid(a.B, a.H * a.max_new, (a.d_h + 31) / 32);
-  return launch_pdl(paged_merge_seq_kernel, grid, dim3(32 * npg), 0, st, a);
+// Both kinds in one launch: blocks [0, seq_blocks) take sequences, the rest row blocks.
+__global__ void __launch_bounds__(1024)
+    paged_merge_kernel(const PagedArgs s, const PagedArgs r, int seq_blocks, int Hp, int chunks, int rows_y,
+                       int M) {
+  pdl_trigger();   // successors wait for this kernel before they read its outputs
+  pdl_wait();
+  int i = blockIdx.x;
+  if (i < seq_blocks) {
+    const int z = i % chunks;
+    i /= chunks;
+    merge_seq(s, i / Hp, i % Hp, z, Hp);
+  } else {
+    i -= seq_blocks;
+    merge_rows(r, i / rows_y, i % rows_y, M);
+  }
 }
 
-cudaError_t launch_paged_merge_rows(const PagedArgs& a, int M, cudaStream_t st) {
-  const long long most = (long long)a.max_new * a.hpr;   // rows of the fullest block
-  const dim3 grid(a.grid, (unsigned)(((most < M ? most : M) + 7) / 8));
-  if (M == kPagedTcRows) return launch_pdl(paged_merge_rows_kernel<kPagedTcRows>, grid, dim3(256), 0, st, a);
-  return launch_pdl(paged_merge_rows_kernel<kPagedSimtRows>, grid, dim3(256), 0, st, a);
+}  // namespace
+
+cudaError_t launch_paged_merge(const PagedArgs* s, const PagedArgs* r, int M, cudaStream_t st) {
+  int npg = 8, Hp = 1, chunks = 1, rows_y = 1;
+  long long seq_blocks = 0, row_blocks = 0;
+  if (s) {
+    // a sequence has about grid / B + 1 pieces (ragged batches: more for the long ones)
+    const int per_seq = s->grid / s->B + 2;
+    npg = (per_seq + kPieces - 1) / kPieces;
+    npg = npg < 1 ? 1 : (npg > 32 ? 32 : npg);
+    if (r && npg < 8) npg = 8;
+    Hp = s->H * s->max_new;
+    chunks = (s->d_h + 31) / 32;
+    seq_blocks = (long long)s->B * Hp * chunks;
+  }
+  if (r) {
+    const long long most = (long long)r->max_new * r->hpr;   // rows of the fullest block
+    rows_y = (int)(((most < M ? most : M) + npg - 1) / npg);
+    row_blocks = (long long)r->grid * rows_y;
+  }
+  const PagedArgs none{};
+  return launch_pdl(paged_merge_kernel, dim3((unsigned)(seq_blocks + row_blocks)), dim3(32 * npg), 0, st,
+                    s ? *s : none, r ? *r : none, (int)seq_blocks, Hp, chunks, rows_y, M);
 }
 
 }  // namespace gva

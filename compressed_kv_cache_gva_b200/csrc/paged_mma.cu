@@ -124,8 +124,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     if (C::DRP) prefetch_tmap(&tm_kr);
   }
   // queries, lengths, tables and cache rows may come from the kernels before
-  pdl_wait();
-  pdl_trigger();   // the merge waits for this kernel before it reads
+  pdl_enter(a);
   // tiles of a sequence: one (masked) tile where it has no key
   auto tiles = [](const SeqRows& s) -> long long {
     return s.n == 0 ? 0 : max(1, (s.L + C::TT - 1) / C::TT);

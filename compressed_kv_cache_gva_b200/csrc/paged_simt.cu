@@ -7,6 +7,8 @@
 // Thread (r, x) of 16 x 16: scores of row r with keys x and x + 16, online softmax
 // over the row's 16 threads, then output columns x, x + 16, ... of row r.
 // Bound by the fp32 FMAs and their shared-memory operands, about one load per FMA.
+#include <type_traits>
+
 #include "launch.h"
 #include "paged.cuh"
 
@@ -15,7 +17,7 @@ namespace gva {
 namespace {
 
 constexpr int kM = kPagedSimtRows, kTK = 32, kThreads = 256;
-constexpr int kMaxD = 512, kCols = kMaxD / 16;
+constexpr int kMaxD = 512;
 
 struct SimtSmem {
   int ldq, ldv, ldr;
@@ -38,7 +40,7 @@ __host__ __device__ inline SimtSmem simt_smem(int B, int d_h, int d_r) {
   return s;
 }
 
-template <typename T>
+template <typename T, int COLS>   // output columns per thread: d_h <= 16 COLS
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a, const SimtSmem S) {
   extern __shared__ __align__(16) unsigned char sm[];
   float* Qs = reinterpret_cast<float*>(sm + S.q);
@@ -55,23 +57,40 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
   const T* V = reinterpret_cast<const T*>(a.V);
   const T* KR = reinterpret_cast<const T*>(a.KR);
   // queries, lengths, tables and cache rows may come from the kernels before
-  pdl_wait();
-  pdl_trigger();   // the merge waits for this kernel before it reads
+  pdl_enter(a);
   if (blockIdx.x == 0 && a.flag_errors) flag_bad_sequences(a);
   const RowBlocks<kM, kTK> blocks{a};
-  const long long total =
-      block_scan(a.B, [&](int b) { return blocks.units(b); }, prefix, wtmp);
-  if (total >= (1ll << 31) && tid == 0) atomicOr(a.status, GVA_DEVERR_RANGE);
-  const TileSplit ts = make_split(prefix[a.B], (int)gridDim.x, 0);
-  if (tid == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-  RowWalk<kM, kTK> walk{blocks, prefix, ts.first(blockIdx.x), ts.first(blockIdx.x + 1), {}, {}};
-  if (tid < 32) {
-    const bool any = walk.first();
-    if (tid == 0) {
-      more = any;
-      piece = walk.p;
+  TileSplit ts;
+  long long total;
+  RowWalk<kM, kTK> walk{blocks, prefix, 0, 0, {}, {}};
+  if (a.B <= kLaneBatch) {
+    const LaneBatch t = lane_batch(a, [&](const SeqRows& s) { return blocks.units(s); });
+    total = t.total;
+    ts = make_split(total < (1ll << 31) ? (int)total : 0, (int)gridDim.x, 0);
+    walk.u = ts.first(blockIdx.x);
+    walk.end = ts.first(blockIdx.x + 1);
+    if (tid < 32) {
+      const bool any = walk.first(t);
+      if (tid == 0) {
+        more = any;
+        piece = walk.p;
+      }
+    }
+  } else {
+    total = block_scan(a.B, [&](int b) { return blocks.units(b); }, prefix, wtmp);
+    ts = make_split(prefix[a.B], (int)gridDim.x, 0);
+    walk.u = ts.first(blockIdx.x);
+    walk.end = ts.first(blockIdx.x + 1);
+    if (tid < 32) {
+      const bool any = walk.first();
+      if (tid == 0) {
+        more = any;
+        piece = walk.p;
+      }
     }
   }
+  if (total >= (1ll << 31) && tid == 0) atomicOr(a.status, GVA_DEVERR_RANGE);
+  if (tid == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   __syncthreads();
   while (more) {
     const RowPiece p = piece;
@@ -86,9 +105,9 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
     }
     const int qi = (row0 + r) / hpr, head = p.g * hpr + (row0 + r) % hpr;
     const int lim = s.L - s.n + qi;   // last key of this row
-    float m = -INFINITY, l = 0.f, o[kCols];
+    float m = -INFINITY, l = 0.f, o[COLS];
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) o[i] = 0.f;
+    for (int i = 0; i < COLS; ++i) o[i] = 0.f;
     for (int k = p.k0; k < p.k1; ++k) {
       const int t0 = k * kTK;
       __syncthreads();   // the previous tile (and this block's queries) are in place / free
@@ -127,12 +146,12 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
       Ps[r * (kTK + 1) + x + 16] = p1;
       __syncwarp();   // a row's 16 threads are in one warp
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) o[i] *= al;
+      for (int i = 0; i < COLS; ++i) o[i] *= al;
       for (int t = 0; t < kTK; ++t) {
         const float pt = Ps[r * (kTK + 1) + t];
         const float* v = Vs + t * S.ldv + x;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i)
+        for (int i = 0; i < COLS; ++i)
           if (x + 16 * i < d_h) o[i] = fmaf(pt, v[16 * i], o[i]);
       }
       __syncwarp();
@@ -143,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
         const long long orow = (long long)(s.r0 + qi) * a.H + head;
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) {
+        for (int i = 0; i < COLS; ++i) {
           const int c = x + 16 * i;
           if (c >= d_h) break;
           if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[orow * d_h + c] = __float2bfloat16_rn(o[i] * inv);
@@ -154,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
         const long long slot = piece_slot(p, blockIdx.x);
         float* po = a.part_o + (slot * kM + r) * d_h;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) {
+        for (int i = 0; i < COLS; ++i) {
           const int c = x + 16 * i;
           if (c >= d_h) break;
           po[c] = o[i];
@@ -173,6 +192,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
     }
     __syncthreads();
   }
+  pdl_leave(a);
 }
 
 }  // namespace
@@ -195,10 +215,18 @@ int paged_simt_grid(const gva_shape_t& sh, int n_rows, int num_sms, long long ma
 
 cudaError_t launch_paged_simt(const gva_shape_t& sh, const PagedArgs& a, cudaStream_t st) {
   const SimtSmem S = simt_smem(sh.B, sh.d_h, sh.d_r);
-  auto k = sh.cache_dtype == GVA_BF16 ? paged_simt_kernel<__nv_bfloat16> : paged_simt_kernel<float>;
-  cudaError_t e = ensure_max_smem(k, S.total);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(a.grid), dim3(kThreads), S.total, st, a, S);
+  auto go = [&](auto k) {
+    const cudaError_t e = ensure_max_smem(k, S.total);
+    return e == cudaSuccess ? launch_pdl(k, dim3(a.grid), dim3(kThreads), S.total, st, a, S) : e;
+  };
+  auto by_type = [&](auto cols) {
+    constexpr int COLS = decltype(cols)::value;
+    return sh.cache_dtype == GVA_BF16 ? go(paged_simt_kernel<__nv_bfloat16, COLS>)
+                                      : go(paged_simt_kernel<float, COLS>);
+  };
+  if (sh.d_h <= 64) return by_type(std::integral_constant<int, 4>{});
+  if (sh.d_h <= 128) return by_type(std::integral_constant<int, 8>{});
+  return by_type(std::integral_constant<int, 32>{});
 }
 
 }  // namespace gva

@@ -48,6 +48,11 @@ struct PtCfg {
   static constexpr int TK = D_H == 64 && !HILO ? 128 : 64;
   static constexpr int CB = D_H / 64, KS = D_H / 16, RS = DRP / 16;
   static constexpr int QB = MS * D_H * 2;    // q~ hi (or lo): CB blocks of MS rows x 128 B
+  // rows that one warp loads at a time: four 32-byte loads per lane, and one or two of
+  // the positional part
+  static constexpr int GR = D_H == 64 ? 16 : 8;
+  static constexpr int GROUPS = MS / GR, QSTEPS = GR * (D_H / 8) / 32;
+  static_assert(GROUPS * GR == MS, "row groups");
   static constexpr int QRB = DRP ? (MS * DRP * 2 + 1023) / 1024 * 1024 : 0;
   static constexpr int VB = CB * TK * 128;
   static constexpr int KRB = DRP * TK * 2;
@@ -118,56 +123,67 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Queries of a piece -> shared memory: bf16 hi and lo halves, swizzled K-major rows; by
-// threads tid of nthr.  A thread keeps its chunk of 8 elements and steps over rows, four
-// loads of 32 bytes in flight.
-template <class C, int W>   // W: chunks of the part of a row (content, then positional)
-__device__ __forceinline__ void load_query_part(const PagedArgs& a, const float* base, int rows, int row0,
-                                                uint8_t* dst, int half, bool pos, int width, int tid, int nthr) {
-  const int c = tid % W, step = nthr / W;
-  int r = tid / W;
-  const unsigned R = row0 + r, hpr = a.hpr;
-  unsigned qi = R / hpr, h = R - qi * hpr;
-  const unsigned dqi = step / hpr, dh = step - dqi * hpr;
-  const long long dq = C::D_H + a.d_r, token = (long long)a.H * dq;
-  while (r < C::MS) {
-    float4 x[4][2];
+// Queries of a piece -> shared memory: bf16 hi and lo halves, swizzled K-major rows.
+// Groups of GR rows are handed out to warps by a counter (`taken`, which runs on over
+// the pieces; `limit` is the piece's last group): two warps start on the next piece's
+// queries as soon as the last scores of this one are computed, the softmax warps join
+// when they are done.  A lane has four 32-byte loads in flight.
+template <class C, int W, int STEPS>   // W: chunks of 8 elements of the part of a row
+__device__ __forceinline__ void load_query_part(const float* base, int rows, int first, uint32_t row0, unsigned hpr,
+                                                long long token, int dq, uint8_t* dst, int half, bool pos, int width,
+                                                int lane) {
+  const int c = lane % W;
+  float4 x[STEPS][2];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r + u * step < rows && c * 8 < width) {
-        const float* src = base + qi * token + h * dq + c * 8;
-        x[u][0] = *reinterpret_cast<const float4*>(src);
-        x[u][1] = *reinterpret_cast<const float4*>(src + 4);
-      }
-      qi += dqi;
-      h += dh;
-      if (h >= hpr) {
-        h -= hpr;
-        ++qi;
-      }
+  for (int u = 0; u < STEPS; ++u) {
+    const int i = u * (32 / W) + lane / W, r = first + i;
+    x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < C::GR && r < rows && c * 8 < width) {
+      const unsigned R = row0 + r, qi = R / hpr;
+      const float* src = base + qi * token + (R - qi * hpr) * dq + c * 8;
+      x[u][0] = *reinterpret_cast<const float4*>(src);
+      x[u][1] = *reinterpret_cast<const float4*>(src + 4);
     }
+  }
 #pragma unroll
-    for (int u = 0; u < 4; ++u, r += step) {
-      if (r >= C::MS) break;
-      const float y[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
-      uint4 lo;
-      const uint4 hi = split_bf16(y, lo);
-      const uint32_t o = pos ? sw_pos<C::DRP>(r, c) : (c / 8) * (C::MS * 128) + sw128(r, c % 8);
-      *reinterpret_cast<uint4*>(dst + o) = hi;
-      *reinterpret_cast<uint4*>(dst + o + half) = lo;
-    }
+  for (int u = 0; u < STEPS; ++u) {
+    const int i = u * (32 / W) + lane / W, r = first + i;
+    if (i >= C::GR) break;
+    const float y[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+    uint4 lo;
+    const uint4 hi = split_bf16(y, lo);
+    const uint32_t o = pos ? sw_pos<C::DRP>(r, c) : (c / 8) * (C::MS * 128) + sw128(r, c % 8);
+    *reinterpret_cast<uint4*>(dst + o) = hi;
+    *reinterpret_cast<uint4*>(dst + o + half) = lo;
   }
 }
 template <class C>
 __device__ __forceinline__ void load_queries(const PagedArgs& a, const RowPiece& p, const SeqRows& s,
-                                             uint8_t* sm, int tid, int nthr) {
+                                             uint8_t* sm, int* taken, int limit, uint32_t q_full, int lane) {
   const int row0 = p.rb * C::M, rows = min(C::MS, s.n * a.hpr - row0), dq = C::D_H + a.d_r;
   const float* base = a.q_abs + ((long long)s.r0 * a.H + p.g * a.hpr) * dq;
-  load_query_part<C, C::D_H / 8>(a, base, rows, row0, sm, C::QB, false, C::D_H, tid, nthr);
-  if constexpr (C::DRP > 0)
-    load_query_part<C, C::DRP / 8>(a, base + C::D_H, rows, row0, sm + C::OFF_QR, C::QRB, true, a.d_r, tid, nthr);
-  fence_proxy_async_smem();   // the queries are read by the tensor core (async proxy)
+  const long long token = (long long)a.H * dq;
+  for (;;) {
+    int t = 0;
+    if (lane == 0) {
+      t = *reinterpret_cast<volatile int*>(taken);
+      while (t < limit) {
+        const int was = atomicCAS(taken, t, t + 1);
+        if (was == t) break;
+        t = was;
+      }
+    }
+    t = __shfl_sync(0xffffffffu, t, 0);
+    if (t >= limit) break;
+    const int first = (t - (limit - C::GROUPS)) * C::GR;
+    load_query_part<C, C::D_H / 8, C::QSTEPS>(base, rows, first, row0, a.hpr, token, dq, sm, C::QB, false, C::D_H, lane);
+    if constexpr (C::DRP > 0)
+      load_query_part<C, C::DRP / 8, (C::GR * (C::DRP / 8) + 31) / 32>(base + C::D_H, rows, first, row0, a.hpr, token, dq,
+                                                                sm + C::OFF_QR, C::QRB, true, a.d_r, lane);
+    fence_proxy_async_smem();   // the queries are read by the tensor core (async proxy)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
+  }
 }
 // Ask L2 for the queries of a piece that is loaded later.
 template <class C>
@@ -206,6 +222,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   long long* wtmp = reinterpret_cast<long long*>(
       (reinterpret_cast<uintptr_t>(prefix + 2 * a.B + 1) + 15) & ~uintptr_t(15));
   int* units = prefix + a.B + 1;
+  __shared__ int taken;   // query row groups taken so far
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hpr = a.hpr;
   if (threadIdx.x == 0) {
@@ -217,9 +234,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     mbar_init(s_free, 4);
     mbar_init(p_full, 4);
     mbar_init(pv_done, 1);
-    mbar_init(q_full, 2);
+    mbar_init(q_full, C::GROUPS);
     mbar_init(q_free, 1);
     mbar_init(fin, 1);
+    taken = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -231,8 +249,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     if (C::DRP) prefetch_tmap(&tm_kr);
   }
   // queries, lengths, tables and cache rows may come from the kernels before
-  pdl_wait();
-  pdl_trigger();   // the merge waits for this kernel before it reads
+  pdl_enter(a);
   if (blockIdx.x == 0 && a.flag_errors) flag_bad_sequences(a);
   const RowBlocks<C::M, C::TK> blocks{a};
   // Every role walks the CTA's pieces by itself.
@@ -384,13 +401,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         if (i > 0) {
           prefetch_queries<C>(a, p, s, threadIdx.x - 64, 64);
           ok = ok && mbar_wait(q_free, (i - 1) & 1, a.status);
-          load_queries<C>(a, p, s, sm, threadIdx.x - 64, 64);
-        } else {   // nothing else to do yet: the softmax warps help
-          load_queries<C>(a, p, s, sm, threadIdx.x - 64, 192);
-          named_bar_sync(1, 192);
+          ok = __all_sync(0xffffffffu, ok);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
+        load_queries<C>(a, p, s, sm, &taken, (i + 1) * C::GROUPS, q_full, lane);
       }
     }
   } else {
@@ -400,9 +413,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     // A row of scores takes most of the registers: the walk waits in shared memory.
     __shared__ SoftmaxPiece pieces[4];
     SoftmaxPiece& sp = pieces[quarter];
+    int q_limit = C::GROUPS;
     if (more) {
-      load_queries<C>(a, p, s, sm, threadIdx.x - 64, 192);
-      named_bar_sync(1, 192);
+      load_queries<C>(a, p, s, sm, &taken, q_limit, q_full, lane);
       if (lane == 0) sp = SoftmaxPiece{walk.p, walk.s, walk.u, walk.end};
     }
     __syncwarp();
@@ -456,8 +469,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float2 e = add2(make_float2(x[16 * q + 2 * i], x[16 * q + 2 * i + 1]), neg);
-              e.x = ex2(e.x);
-              e.y = ex2(e.y);
+              e = make_float2(ex2(e.x), ex2(e.y));
               sum[i & 3] = add2(sum[i & 3], e);
               if constexpr (C::HILO) {
                 const float hx = bf16_round(e.x), hy = bf16_round(e.y);
@@ -523,6 +535,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         const int R = row0 + r, qi = R / hpr, head = sp.p.g * hpr + R % hpr;
         const long long orow = (long long)(sp.s.r0 + qi) * a.H + head;
         const long long prt = (long long)piece_slot(sp.p, blockIdx.x) * C::M + r;
+        if (m == -INFINITY) l = 0.f;   // no key: exactly 0, whatever the masked scores left
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
         for (int q = 0; q < C::D_H / 64; ++q) {
@@ -569,6 +582,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       }
       __syncwarp();
       more = sp.more;
+      q_limit += C::GROUPS;
+      if (more) load_queries<C>(a, sp.p, sp.s, sm, &taken, q_limit, q_full, lane);
       tc::fence_before();   // O has been read: the P of the next piece orders its first P.V behind
     }
   }
@@ -580,6 +595,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     tc::fence_after();
     tc::dealloc(tmem, C::TMEM_COLS);
   }
+  pdl_leave(a);
 }
 
 // Visit the configuration of (d_h, padded d_r, output type, rows of a block).
