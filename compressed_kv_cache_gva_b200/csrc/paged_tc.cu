@@ -3,7 +3,7 @@
 //
 // A block is M = 128 query rows (new token x head of a value group) of one sequence:
 //   S[M x TK] = Q~_hi V^T + Q~_lo V^T + Qr_hi Kr^T + Qr_lo Kr^T   (tcgen05, TMEM)
-//   online softmax of the rows, fp32, base 2                       (4 warps)
+//   online softmax of the rows, fp32, base 2                       (4 or 8 warps)
 //   O[M x d_h] = alpha O + P V                                     (tcgen05, TMEM)
 // The fp32 query is split in bf16 hi + lo, so the scores keep ~16 bits.  P is bf16
 // where the output is (2^-9 relative, below the output's own rounding) and hi + lo
@@ -17,9 +17,9 @@
 //
 // Roles: warp 0 streams tiles with 2-D TMA loads, one box per page (or part of one),
 // its lanes holding the cache rows of the next 32 boxes; one thread of warp 1 issues
-// every MMA; warps 4..7 (a TMEM lane quarter each) do the softmax, write P back to
-// tensor memory (the A operand of the value product) and rescale O only when a row's
-// maximum grew by more than 2^8.  While they exponentiate tile k, the MMA thread has
+// every MMA; warps 2 and 3 load the queries of the next piece; the warps from 4 on (one or
+// two per TMEM lane quarter) do the softmax, write P back to tensor memory (the A operand of the
+// value product) and rescale O only when a row's maximum grew by more than 2^8.  While they exponentiate tile k, the MMA thread has
 // the scores of tile k + 1 computed.  All ring and buffer barriers count tiles over the
 // whole CTA, so they run on across pieces.
 #include <atomic>
@@ -42,10 +42,18 @@ struct PtCfg {
   static constexpr int MS = MS_;
   static constexpr bool HILO = HILO_;        // P in two bf16 halves (float32 output)
   static constexpr int M = kPagedTcRows;
-  // Keys per tile.  S, P and O of two CTAs share the SM's 512 tensor-memory columns:
-  // 128 + 64 + 64 with d_h = 64, 64 + 32 + 128 with d_h = 128, 64 + 64 + d_h where P
-  // has two halves.  Longer tiles have fewer hand-offs per key.
-  static constexpr int TK = D_H == 64 && !HILO ? 128 : 64;
+  // Keys per tile and score buffers, by what tensor memory holds (512 columns an SM):
+  // d_h = 64: S 128, P 64, O 64 in the 256 columns of one of two CTAs per SM (S 64, P 32
+  // + 32 where P has two halves); d_h = 128: 2 x S 128, P 64 (+ 64), O 128 of one CTA.
+  // 128-key tiles: the score products of 64 keys read 6 KB of shared memory for 32
+  // clocks of arithmetic, above its 128 bytes a clock; those of 128 keys do not.
+  static constexpr int TK = D_H == 64 && HILO ? 64 : 128;
+  static constexpr int NS = D_H == 64 ? 1 : 2;
+  // Softmax warps per 32 rows.  The one CTA of d_h = 128 needs two, half of the keys
+  // each, to keep up with the products (mixed d_h = 128 step 105 -> 95 us); with two CTAs
+  // an SM one each does as well and costs no exchange (d_h = 64 chunk 168 against 174 us).
+  static constexpr int NH = D_H == 64 ? 1 : 2;
+  static constexpr int HK = TK / NH, HD = D_H / NH;   // keys and output columns of a softmax warp
   static constexpr int CB = D_H / 64, KS = D_H / 16, RS = DRP / 16;
   static constexpr int QB = MS * D_H * 2;    // q~ hi (or lo): CB blocks of MS rows x 128 B
   // rows that one warp loads at a time: four 32-byte loads per lane, and one or two of
@@ -58,32 +66,31 @@ struct PtCfg {
   static constexpr int KRB = DRP * TK * 2;
   static constexpr int STAGE = VB + (KRB + 1023) / 1024 * 1024;
   static constexpr int OFF_QR = 2 * QB, OFF_RING = OFF_QR + 2 * QRB;
-  // as many stages as let two CTAs share an SM, or one where not even two stages fit
-  static constexpr int HALF = 113 * 1024 - 2048, WHOLE = 227 * 1024 - 2048;
-  static constexpr bool TWO = OFF_RING + 2 * STAGE <= HALF;
-  static constexpr int STAGES_RAW = ((TWO ? HALF : WHOLE) - OFF_RING) / STAGE;
+  // as many stages as fit beside the CTAs of an SM
+  static constexpr int PER_SM = D_H == 64 ? 2 : 1;
+  static constexpr int ROOM = (PER_SM == 2 ? 113 : 227) * 1024 - 4096;
+  static constexpr int STAGES_RAW = (ROOM - OFF_RING) / STAGE;
   static constexpr int STAGES = STAGES_RAW > 6 ? 6 : STAGES_RAW;
-  static constexpr int PER_SM = TWO ? 2 : 1;
   static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
-  // full[S], empty[S], s_full, s_free, p_full, pv_done, q_full, q_free, fin
-  static constexpr int NBAR = 2 * STAGES + 7;
+  // full[S], empty[S], s_full[2], s_free[2], p_full, pv_done, q_full, q_free, fin
+  static constexpr int NBAR = 2 * STAGES + 9;
   // the unit prefix of the prologue lies where the queries and the ring are later
   static constexpr int SMEM = 1024 + OFF_BAR + NBAR * 8 + 8;
   static_assert(OFF_BAR >= (int)sizeof(int) * (2 * kMaxBatch + 1) + 16 + 33 * 8, "unit prefix");
   // rows past MS are read up to a full block's size behind each operand
   static_assert(SMEM - 1024 >= 2 * QB + 2 * QRB + M * 128, "operand reads stay inside");
   static_assert(STAGES >= 2 && SMEM <= 227 * 1024, "shared memory");
-  static constexpr uint32_t S_COL = 0, P_COL = TK, P_COLS = TK / 2;
-  static constexpr uint32_t O_COL = D_H == 64 && !HILO ? 192 : 128;
-  static constexpr uint32_t TMEM_COLS = 256;
-  static_assert(P_COL + P_COLS * (HILO ? 2 : 1) <= O_COL && O_COL + D_H <= TMEM_COLS, "tensor memory");
+  static constexpr uint32_t S_COL = 0, P_COL = NS * TK, P_COLS = TK / 2;
+  static constexpr uint32_t O_COL = P_COL + P_COLS * (HILO ? 2 : 1);
+  static constexpr uint32_t TMEM_COLS = 512 / PER_SM;
+  static_assert(O_COL + D_H <= TMEM_COLS, "tensor memory");
   static constexpr uint32_t TX = VB + KRB;
-  static constexpr int THREADS = 256;
+  static constexpr int THREADS = 128 + 128 * NH;
   static constexpr uint32_t SW_R = DRP == 32 ? tc::kSw64 : tc::kSw32;
   static constexpr uint32_t SBO_R = DRP * 2 * 8;
-  // A row of 128 scores does not fit the 128 registers that two CTAs leave a thread:
-  // the softmax warps take theirs from the other four (88 + 168 = 2 x 128)
-  static constexpr bool SPLIT_REGS = TK == 128 && PER_SM == 2;
+  // Two CTAs of 256 threads leave 128 registers a thread; a softmax warp holds 128 scores
+  // a lane, so those warps take registers from the other four (88 + 168 = 2 x 128).
+  static constexpr bool SPLIT_REGS = PER_SM == 2 && HK == 128;
 };
 
 // 16-byte chunk of a row in a swizzled K-major tile (rows of 128, 64 or 32 bytes).
@@ -214,8 +221,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   const uint32_t sb = smem_u32(sm);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   const uint32_t full = smem_u32(bars), empty = full + 8 * C::STAGES;
-  const uint32_t s_full = empty + 8 * C::STAGES, s_free = s_full + 8;
-  const uint32_t p_full = s_free + 8, pv_done = p_full + 8, q_full = pv_done + 8;
+  const uint32_t s_full = empty + 8 * C::STAGES, s_free = s_full + 16;
+  const uint32_t p_full = s_free + 16, pv_done = p_full + 8, q_full = pv_done + 8;
   const uint32_t q_free = q_full + 8, fin = q_free + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   int* prefix = reinterpret_cast<int*>(sm);
@@ -230,9 +237,11 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, 4);
-    mbar_init(p_full, 4);
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(s_free + 8 * i, 4 * C::NH);
+    }
+    mbar_init(p_full, 4 * C::NH);
     mbar_init(pv_done, 1);
     mbar_init(q_full, C::GROUPS);
     mbar_init(q_free, 1);
@@ -347,10 +356,11 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
             if (k < nk) {
               const int kk = kt + k, sg = kk % C::STAGES;
               ok = ok && mbar_wait(full + 8 * sg, (kk / C::STAGES) & 1, a.status);
-              if (kk >= 1) ok = ok && mbar_wait(s_free, (kk - 1) & 1, a.status);
+              const int sb_ = kk % C::NS;   // score buffer
+              if (kk >= C::NS) ok = ok && mbar_wait(s_free + 8 * sb_, (kk / C::NS - 1) & 1, a.status);
               tc::fence_after();
               if (ok) {
-                const uint32_t d = tmem + C::S_COL, vt = sb + C::OFF_RING + sg * C::STAGE;
+                const uint32_t d = tmem + C::S_COL + sb_ * C::TK, vt = sb + C::OFF_RING + sg * C::STAGE;
 #pragma unroll
                 for (int ks = 0; ks < C::KS; ++ks) {
                   const uint32_t kb = (ks >> 2) * (C::MS * 128) + (ks & 3) * 32;
@@ -367,7 +377,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
                                idS, 1);
                 }
               }
-              tc::commit(s_full);
+              tc::commit(s_full + 8 * sb_);
               if (k == nk - 1) tc::commit(q_free);   // the piece's queries have been read
             }
             if (k >= 1) {   // P.V of the tile before
@@ -408,11 +418,14 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     }
   } else {
     if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-    const int quarter = warp & 3, r = 32 * quarter + lane;
+    // One warp per lane quarter, or two that share its 32 rows, half of a tile's keys and
+    // of the output columns each.
+    const int quarter = warp & 3, half = (warp - 4) >> 2, r = 32 * quarter + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
+    __shared__ float row_x[2][C::NH][C::M];   // exchange between two halves: [tile parity][half][row]
     // A row of scores takes most of the registers: the walk waits in shared memory.
-    __shared__ SoftmaxPiece pieces[4];
-    SoftmaxPiece& sp = pieces[quarter];
+    __shared__ SoftmaxPiece pieces[4 * C::NH];
+    SoftmaxPiece& sp = pieces[warp - 4];
     int q_limit = C::GROUPS;
     if (more) {
       load_queries<C>(a, p, s, sm, &taken, q_limit, q_full, lane);
@@ -423,37 +436,43 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       const int nk = sp.p.k1 - sp.p.k0, k0 = sp.p.k0, row0 = sp.p.rb * C::M;
       const int L = sp.s.L, first_lim = sp.s.L - sp.s.n, rows = min(C::M, sp.s.n * hpr - row0);
       // ---------------------------------------------------------- softmax, P, O rescale, output
-      // idle: no row of this warp counts.  A row of P meets only its own row of O, so
+      // idle: no row of this quarter counts.  A row of P meets only its own row of O, so
       // what idle lanes of the tensor memory hold does not matter.
       const bool valid = r < rows, idle = 32 * quarter >= rows;
-            const int lim = first_lim + (row0 + r) / hpr;                // last key of this row
+      const int lim = first_lim + (row0 + r) / hpr;                // last key of this row
       const int kv_all = first_lim + row0 / hpr + 1;               // keys every row sees
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;   // the row's reference; this half's sum
       for (int k = 0; k < nk; ++k) {
-        const int kk = kt + k, t0 = (k0 + k) * C::TK;
-        ok = ok && mbar_wait(s_full, kk & 1, a.status);
+        const int kk = kt + k, sbuf = kk % C::NS, t0 = (k0 + k) * C::TK;
+        ok = ok && mbar_wait(s_full + 8 * sbuf, (kk / C::NS) & 1, a.status);
         tc::fence_after();
         if (!idle) {
-          float x[C::TK];
+          float x[C::HK];
 #pragma unroll
-          for (int q = 0; q < C::TK / 32; ++q) tc::ld32(trow + C::S_COL + q * 32, x + q * 32);
+          for (int q = 0; q < C::HK / 32; ++q)
+            tc::ld32(trow + C::S_COL + sbuf * C::TK + half * C::HK + q * 32, x + q * 32);
           tc::wait_ld();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(s_free);
+          if (lane == 0) mbar_arrive(s_free + 8 * sbuf);
           // four running maxima (and sums below): one dependent chain would cost more
           // than the operations themselves
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           if (!ok || t0 + C::TK > kv_all) {   // some row does not see the whole tile
-            const int vis = ok && valid ? min(lim + 1, L) - t0 : 0;
+            const int vis = (ok && valid ? min(lim + 1, L) - t0 : 0) - half * C::HK;
 #pragma unroll
-            for (int j = 0; j < C::TK; ++j) x[j] = j < vis ? x[j] : -INFINITY;
+            for (int j = 0; j < C::HK; ++j) x[j] = j < vis ? x[j] : -INFINITY;
           }
 #pragma unroll
-          for (int j = 0; j < C::TK; j += 8)
+          for (int j = 0; j < C::HK; j += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i) mx4[i] = max3(mx4[i], x[j + 2 * i], x[j + 2 * i + 1]);
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          if constexpr (C::NH == 2) {
+            row_x[kk & 1][half][r] = mx;
+            named_bar_sync(1 + quarter, 64);
+            mx = fmaxf(mx, row_x[kk & 1][half ^ 1][r]);
+          }
           // a row keeps the maximum its exponentials are taken against until a tile
           // exceeds it by more than 8 (log2 units): P <= 2^8, and O is touched only then
           const bool grow = mx > m + 8.f;
@@ -464,7 +483,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           const float2 neg = make_float2(-ms, -ms);
           float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-          for (int q = 0; q < C::TK / 16; ++q) {   // 16 keys at a time
+          for (int q = 0; q < C::HK / 16; ++q) {   // 16 keys at a time
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -483,27 +502,29 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
               ok = ok && mbar_wait(pv_done, (kk - 1) & 1, a.status);
               tc::fence_after();
             }
-            tc::st8u(trow + C::P_COL + q * 8, hi);
-            if constexpr (C::HILO) tc::st8u(trow + C::P_COL + C::P_COLS + q * 8, lo);
+            const uint32_t pc = trow + C::P_COL + half * (C::HK / 2) + q * 8;
+            tc::st8u(pc, hi);
+            if constexpr (C::HILO) tc::st8u(pc + C::P_COLS, lo);
           }
           l = l * alpha + (((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
                            ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y)));
           // O *= alpha before this tile's P.V
           if (k >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
-            for (int q4 = 0; q4 < C::D_H / 16; ++q4) {
+            for (int q4 = 0; q4 < C::HD / 16; ++q4) {
               float o[16];
-              tc::ld16(trow + C::O_COL + q4 * 16, o);
+              const uint32_t oc = trow + C::O_COL + half * C::HD + q4 * 16;
+              tc::ld16(oc, o);
               tc::wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] *= alpha;
-              tc::st16(trow + C::O_COL + q4 * 16, o);
+              tc::st16(oc, o);
             }
           }
           tc::wait_st();
         } else {
           __syncwarp();
-          if (lane == 0) mbar_arrive(s_free);
+          if (lane == 0) mbar_arrive(s_free + 8 * sbuf);
           // keep step with the warps that write P: an arrival for this tile must not
           // count for the one before
           if (kk >= 1) ok = ok && mbar_wait(pv_done, (kk - 1) & 1, a.status);
@@ -513,7 +534,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         if (t0 + C::TK > L) {
           uint8_t* vt = sm + C::OFF_RING + (kk % C::STAGES) * C::STAGE;
           const int r_lo = max(L - t0, 0), nz = (C::TK - r_lo) * 8;   // 16-byte chunks per block
-          for (int e = r; e < nz * C::CB; e += 128) {
+          for (int e = (int)threadIdx.x - 128; e < nz * C::CB; e += 128 * C::NH) {
             const int c = e / nz, i = e % nz;
             *reinterpret_cast<uint4*>(vt + c * C::TK * 128 + (r_lo + i / 8) * 128 + (i % 8) * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -531,42 +552,49 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!idle) {
+        if constexpr (C::NH == 2) {   // the halves' sums, through the buffer of the next tile
+          const int xb = (kt + nk) & 1;
+          row_x[xb][half][r] = l;
+          named_bar_sync(1 + quarter, 64);
+          l += row_x[xb][half ^ 1][r];
+          named_bar_sync(1 + quarter, 64);
+        }
         const bool whole = nk == sp.p.nt;
         const int R = row0 + r, qi = R / hpr, head = sp.p.g * hpr + R % hpr;
         const long long orow = (long long)(sp.s.r0 + qi) * a.H + head;
         const long long prt = (long long)piece_slot(sp.p, blockIdx.x) * C::M + r;
-        if (m == -INFINITY) l = 0.f;   // no key: exactly 0, whatever the masked scores left
         const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int d0 = half * C::HD;
 #pragma unroll
-        for (int q = 0; q < C::D_H / 64; ++q) {
-          float o[64];
-          tc::ld32(trow + C::O_COL + q * 64, o);
-          tc::ld32(trow + C::O_COL + q * 64 + 32, o + 32);
+        for (int q = 0; q < C::HD / 32; ++q) {
+          float o[32];
+          tc::ld32(trow + C::O_COL + d0 + q * 32, o);
           tc::wait_ld();
           if (valid && ok) {
             if (!whole) {
-              float4* dst = reinterpret_cast<float4*>(a.part_o + prt * C::D_H + q * 64);
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            } else if (a.out_bf16) {
-              uint4* dst =
-                  reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * C::D_H + q * 64);
+              float4* dst = reinterpret_cast<float4*>(a.part_o + prt * C::D_H + d0 + q * 32);
 #pragma unroll
               for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            } else if (a.out_bf16) {
+              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * C::D_H + d0 +
+                                                    q * 32);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
                 dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
                                     pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                                     pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
                                     pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
             } else {
-              float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * C::D_H + q * 64);
+              float4* dst =
+                  reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * C::D_H + d0 + q * 32);
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
+              for (int i = 0; i < 8; ++i)
                 dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
             }
           }
         }
-        if (valid && ok) {
+        if (valid && ok && half == 0) {
           if (!whole) a.part_ml[prt] = make_float2(m, l);
           else if (a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
         }
