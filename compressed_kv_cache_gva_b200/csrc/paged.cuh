@@ -234,6 +234,14 @@ struct RowWalk {
   }
 };
 
+// Record of a block that this CTA starts and does not end: the number of its pieces,
+// and its rows (q row of its sequence, query rows of the block).
+__device__ __forceinline__ void write_row_meta(const PagedArgs& a, int pieces, const RowPiece& p,
+                                               const SeqRows& s, int M) {
+  a.meta[2 * blockIdx.x] = make_int4(pieces, p.b, p.g, p.rb);
+  a.meta[2 * blockIdx.x + 1] = make_int4(s.r0, s.n * a.hpr - p.rb * M, 0, 0);
+}
+
 // Where a piece's partial state goes: a CTA leaves at most one block that it did not
 // start (slot 2 cta) and one that it started and does not end (slot 2 cta + 1).
 __device__ __forceinline__ int piece_slot(const RowPiece& p, int cta) {

@@ -100,7 +100,7 @@ gva_status_t plan_paged(const gva_shape_t& sh, int page, int n_rows, int max_new
     const int M = p->rows == PagedPlan::kTc ? gva::kPagedTcRows : gva::kPagedSimtRows;
     p->rows_grid = p->rows == PagedPlan::kTc ? gva::paged_tc_grid(sh, n_rows, max_new, sms, max_total)
                                              : gva::paged_simt_grid(sh, n_rows, sms, max_total);
-    p->blk = share(at, p->rows_grid, 2 * (size_t)p->rows_grid, M, sh.d_h);
+    p->blk = share(at, 2 * (size_t)p->rows_grid, 2 * (size_t)p->rows_grid, M, sh.d_h);
     at = p->blk.end;
   }
   p->total = at;

@@ -75,102 +75,117 @@ __device__ __forceinline__ void merge_seq(const PagedArgs& a, int b, int h, int 
   if (lane == 0 && z == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
-// Row blocks cut between CTAs: a warp per row.  Block (i, y) merges rows y W .. y W + W-1
-// (W warps) of the block that CTA i of the split started and did not end; its pieces lie
-// in slots 2 i + 1, 2 (i + 1), 2 (i + 2), ...  A warp holds the piece weights of its row
-// one per lane, then walks the pieces.
+// Row blocks cut between CTAs: the block that CTA i of the split started and did not end;
+// its pieces lie in slots 2 i + 1, 2 (i + 1), 2 (i + 2), ...  A thread merges VEC columns
+// of one row: after the block's record, which names its rows, one round of loads fetches
+// four pieces.  Many small threads: two dependent latencies are nearly all of the time
+// (a warp per row with its piece weights in lanes, or four rows per warp, took 24 and
+// 28 us after a chunk of 8 x 512 tokens).
+constexpr int kRowThreads = 256;
+template <int VEC>
 __device__ __forceinline__ void merge_rows(const PagedArgs& a, int i, int y, int M) {
-  const int r = y * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int4 meta = a.meta[i];
+  const int4 meta = a.meta[2 * i], where = a.meta[2 * i + 1];   // pieces, block, group; first row, rows
+  const unsigned tpr = a.d_h / VEC, e = (unsigned)y * kRowThreads + threadIdx.x;
+  const unsigned r = e / tpr, d = (e - r * tpr) * VEC;
   const int n = meta.x;
-  if (n == 0 || r >= M) return;
-  const int b = meta.y, g = meta.z, R = meta.w * M + r;
-  const int r0 = a.q_start[b], rows = (a.q_start[b + 1] - r0) * a.hpr;
-  if (R >= rows) return;
-  const int d_h = a.d_h;
-  auto slot = [&](int c) { return c == 0 ? 2 * i + 1 : 2 * (i + c); };
-  float mx = -INFINITY;
-  for (int c = lane; c < n; c += 32) mx = fmaxf(mx, a.part_ml[(size_t)slot(c) * M + r].x);
+  if (n == 0 || (int)r >= min(where.y, M)) return;
+  float m = -INFINITY, l = 0.f, o[VEC];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float ms = mx == -INFINITY ? 0.f : mx;
-  const int qi = R / a.hpr, head = g * a.hpr + R % a.hpr;
-  const long long orow = (long long)(r0 + qi) * a.H + head;
-  float L = 0.f;
-  for (int d0 = 0; d0 < d_h; d0 += 128) {   // 4 columns per lane and turn
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
-    L = 0.f;
-    for (int c0 = 0; c0 < n; c0 += 32) {
-      const int c = c0 + lane;
-      float w = 0.f;
-      if (c < n) {
-        const float2 e = a.part_ml[(size_t)slot(c) * M + r];
-        w = ex2(e.x - ms);
-        L = fmaf(w, e.y, L);
-      }
-      const int cn = min(32, n - c0);
-      for (int j = 0; j < cn; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, j);
-        const float* po = a.part_o + ((size_t)slot(c0 + j) * M + r) * d_h;
+  for (int u = 0; u < VEC; ++u) o[u] = 0.f;
+  for (int c0 = 0; c0 < n; c0 += kPieces) {
+    float2 ml[kPieces];
+    float x[kPieces][VEC];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int d = d0 + lane + 32 * u;
-          if (d < d_h) o[u] = fmaf(wj, po[d], o[u]);
+    for (int c = 0; c < kPieces; ++c) {
+      ml[c] = make_float2(-INFINITY, 0.f);
+      if (c0 + c < n) {
+        const size_t row = (size_t)(c0 + c == 0 ? 2 * i + 1 : 2 * (i + c0 + c)) * M + r;
+        ml[c] = a.part_ml[row];
+        if constexpr (VEC == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(a.part_o + row * a.d_h + d);
+          x[c][0] = v.x; x[c][1] = v.y; x[c][2] = v.z; x[c][3] = v.w;
+        } else {
+          x[c][0] = a.part_o[row * a.d_h + d];
         }
       }
     }
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    for (int c = 0; c < kPieces; ++c) {
+      if (ml[c].x == -INFINITY) continue;   // no piece, or one past this row's last key
+      const float mn = fmaxf(m, ml[c].x);
+      const float f = ex2(m - mn), w = ex2(ml[c].x - mn);
+      l = l * f + w * ml[c].y;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int d = d0 + lane + 32 * u;
-      if (d < d_h) store_out(a, orow, d, o[u] * inv);
+      for (int u = 0; u < VEC; ++u) o[u] = o[u] * f + w * x[c][u];
+      m = mn;
     }
   }
-  if (lane == 0 && a.lse) a.lse[orow] = L > 0.f ? (mx + log2f(L)) * kLn2 : -INFINITY;
+  const unsigned R = meta.w * M + r, qi = R / (unsigned)a.hpr;
+  const long long orow = (long long)(where.x + (int)qi) * a.H + meta.z * a.hpr + (int)(R - qi * a.hpr);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int u = 0; u < VEC; ++u) o[u] *= inv;
+  if constexpr (VEC == 4) {
+    if (a.out_bf16)
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * a.d_h + d) =
+          make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+    else
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * a.d_h + d) =
+          make_float4(o[0], o[1], o[2], o[3]);
+  } else {
+    store_out(a, orow, d, o[0]);
+  }
+  if (d == 0 && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Both kinds in one launch: blocks [0, seq_blocks) take sequences, the rest row blocks.
-__global__ void __launch_bounds__(1024)
+// ROWS false: sequences only, with as many warps per block as their pieces want.
+template <bool ROWS>
+__global__ void __launch_bounds__(ROWS ? kRowThreads : 1024)
     paged_merge_kernel(const PagedArgs s, const PagedArgs r, int seq_blocks, int Hp, int chunks, int rows_y,
                        int M) {
   pdl_trigger();   // successors wait for this kernel before they read its outputs
   pdl_wait();
   int i = blockIdx.x;
-  if (i < seq_blocks) {
+  if (!ROWS || i < seq_blocks) {
     const int z = i % chunks;
     i /= chunks;
     merge_seq(s, i / Hp, i % Hp, z, Hp);
-  } else {
+  } else if constexpr (ROWS) {
     i -= seq_blocks;
-    merge_rows(r, i / rows_y, i % rows_y, M);
+    if (r.d_h % 4 == 0) merge_rows<4>(r, i / rows_y, i % rows_y, M);
+    else merge_rows<1>(r, i / rows_y, i % rows_y, M);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_merge(const PagedArgs* s, const PagedArgs* r, int M, cudaStream_t st) {
-  int npg = 8, Hp = 1, chunks = 1, rows_y = 1;
+  int npg = kRowThreads / 32, Hp = 1, chunks = 1, rows_y = 1;
   long long seq_blocks = 0, row_blocks = 0;
   if (s) {
-    // a sequence has about grid / B + 1 pieces (ragged batches: more for the long ones)
-    const int per_seq = s->grid / s->B + 2;
-    npg = (per_seq + kPieces - 1) / kPieces;
-    npg = npg < 1 ? 1 : (npg > 32 ? 32 : npg);
-    if (r && npg < 8) npg = 8;
+    if (!r) {
+      // a sequence has about grid / B + 1 pieces (ragged batches: more for the long ones)
+      const int per_seq = s->grid / s->B + 2;
+      npg = (per_seq + kPieces - 1) / kPieces;
+      npg = npg < 1 ? 1 : (npg > 32 ? 32 : npg);
+    }
     Hp = s->H * s->max_new;
     chunks = (s->d_h + 31) / 32;
     seq_blocks = (long long)s->B * Hp * chunks;
   }
   if (r) {
-    const long long most = (long long)r->max_new * r->hpr;   // rows of the fullest block
-    rows_y = (int)(((most < M ? most : M) + npg - 1) / npg);
+    const long long most = (long long)r->max_new * r->hpr, rows = most < M ? most : M;   // of the fullest block
+    const int tpr = r->d_h % 4 == 0 ? r->d_h / 4 : r->d_h;
+    rows_y = (int)((rows * tpr + kRowThreads - 1) / kRowThreads);
     row_blocks = (long long)r->grid * rows_y;
   }
   const PagedArgs none{};
-  return launch_pdl(paged_merge_kernel, dim3((unsigned)(seq_blocks + row_blocks)), dim3(32 * npg), 0, st,
-                    s ? *s : none, r ? *r : none, (int)seq_blocks, Hp, chunks, rows_y, M);
+  auto go = [&](auto k) {
+    return launch_pdl(k, dim3((unsigned)(seq_blocks + row_blocks)), dim3(32 * npg), 0, st, s ? *s : none,
+                      r ? *r : none, (int)seq_blocks, Hp, chunks, rows_y, M);
+  };
+  return r ? go(paged_merge_kernel<true>) : go(paged_merge_kernel<false>);
 }
 
 }  // namespace gva

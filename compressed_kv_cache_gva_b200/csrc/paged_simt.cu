@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
     }
   }
   if (total >= (1ll << 31) && tid == 0) atomicOr(a.status, GVA_DEVERR_RANGE);
-  if (tid == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   __syncthreads();
   while (more) {
     const RowPiece p = piece;
@@ -184,8 +184,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
     if (tid == 0) {
       if (p.k0 == 0 && !whole) {
         const int start = walk.u;   // the block's first unit, and the CTA that ends it
-        a.meta[blockIdx.x] =
-            make_int4(ts.cta_of(start + p.nt - 1) - (int)blockIdx.x + 1, p.b, p.g, p.rb);
+        write_row_meta(a, ts.cta_of(start + p.nt - 1) - (int)blockIdx.x + 1, p, s, kM);
       }
       more = walk.next();
       piece = walk.p;

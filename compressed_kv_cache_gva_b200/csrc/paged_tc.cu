@@ -56,11 +56,7 @@ struct PtCfg {
   static constexpr int HK = TK / NH, HD = D_H / NH;   // keys and output columns of a softmax warp
   static constexpr int CB = D_H / 64, KS = D_H / 16, RS = DRP / 16;
   static constexpr int QB = MS * D_H * 2;    // q~ hi (or lo): CB blocks of MS rows x 128 B
-  // rows that one warp loads at a time: four 32-byte loads per lane, and one or two of
-  // the positional part
-  static constexpr int GR = D_H == 64 ? 16 : 8;
-  static constexpr int GROUPS = MS / GR, QSTEPS = GR * (D_H / 8) / 32;
-  static_assert(GROUPS * GR == MS, "row groups");
+  static constexpr int GROUPS = MS / 8;      // of query rows, as loaded
   static constexpr int QRB = DRP ? (MS * DRP * 2 + 1023) / 1024 * 1024 : 0;
   static constexpr int VB = CB * TK * 128;
   static constexpr int KRB = DRP * TK * 2;
@@ -131,65 +127,71 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Queries of a piece -> shared memory: bf16 hi and lo halves, swizzled K-major rows.
-// Groups of GR rows are handed out to warps by a counter (`taken`, which runs on over
-// the pieces; `limit` is the piece's last group): two warps start on the next piece's
-// queries as soon as the last scores of this one are computed, the softmax warps join
-// when they are done.  A lane has four 32-byte loads in flight.
-template <class C, int W, int STEPS>   // W: chunks of 8 elements of the part of a row
-__device__ __forceinline__ void load_query_part(const float* base, int rows, int first, uint32_t row0, unsigned hpr,
-                                                long long token, int dq, uint8_t* dst, int half, bool pos, int width,
-                                                int lane) {
-  const int c = lane % W;
-  float4 x[STEPS][2];
-#pragma unroll
-  for (int u = 0; u < STEPS; ++u) {
-    const int i = u * (32 / W) + lane / W, r = first + i;
-    x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < C::GR && r < rows && c * 8 < width) {
+// Warp w of `warps` takes groups w, w + warps, ... of GR = 8 rows, the loads of the next
+// group in flight while it splits and stores one (the latency of L2 is most of the time
+// of two warps).
+template <class C>
+struct QueryGroup {
+  static constexpr int W = C::D_H / 8, STEPS = 8 * W / 32, RW = C::DRP / 8;   // chunks of 8 elements of a row
+  float4 x[STEPS][2], y[2];
+  __device__ __forceinline__ void load(const float* base, int rows, int first, unsigned row0, unsigned hpr,
+                                       long long token, int dq, int d_r, int lane) {
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto row = [&](int r) {
       const unsigned R = row0 + r, qi = R / hpr;
-      const float* src = base + qi * token + (R - qi * hpr) * dq + c * 8;
-      x[u][0] = *reinterpret_cast<const float4*>(src);
-      x[u][1] = *reinterpret_cast<const float4*>(src + 4);
+      return base + qi * token + (R - qi * hpr) * dq;
+    };
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      const int r = first + u * (32 / W) + lane / W;
+      x[u][0] = x[u][1] = zero;
+      if (r < rows) {
+        const float* src = row(r) + (lane % W) * 8;
+        x[u][0] = *reinterpret_cast<const float4*>(src);
+        x[u][1] = *reinterpret_cast<const float4*>(src + 4);
+      }
+    }
+    if constexpr (RW > 0) {
+      const int i = lane / RW, c = lane % RW;
+      y[0] = y[1] = zero;
+      if (i < 8 && first + i < rows && c * 8 < d_r) {
+        const float* src = row(first + i) + C::D_H + c * 8;
+        y[0] = *reinterpret_cast<const float4*>(src);
+        y[1] = *reinterpret_cast<const float4*>(src + 4);
+      }
     }
   }
+  __device__ __forceinline__ void store(uint8_t* sm, int first, int lane) const {
+    auto put = [&](const float4& a, const float4& b, uint8_t* dst, int half) {
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint4 lo;
+      *reinterpret_cast<uint4*>(dst) = split_bf16(v, lo);
+      *reinterpret_cast<uint4*>(dst + half) = lo;
+    };
 #pragma unroll
-  for (int u = 0; u < STEPS; ++u) {
-    const int i = u * (32 / W) + lane / W, r = first + i;
-    if (i >= C::GR) break;
-    const float y[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
-    uint4 lo;
-    const uint4 hi = split_bf16(y, lo);
-    const uint32_t o = pos ? sw_pos<C::DRP>(r, c) : (c / 8) * (C::MS * 128) + sw128(r, c % 8);
-    *reinterpret_cast<uint4*>(dst + o) = hi;
-    *reinterpret_cast<uint4*>(dst + o + half) = lo;
+    for (int u = 0; u < STEPS; ++u) {
+      const int r = first + u * (32 / W) + lane / W, c = lane % W;
+      put(x[u][0], x[u][1], sm + (c / 8) * (C::MS * 128) + sw128(r, c % 8), C::QB);
+    }
+    if constexpr (RW > 0)
+      if (lane / RW < 8) put(y[0], y[1], sm + C::OFF_QR + sw_pos<C::DRP>(first + lane / RW, lane % RW), C::QRB);
   }
-}
+};
 template <class C>
-__device__ __forceinline__ void load_queries(const PagedArgs& a, const RowPiece& p, const SeqRows& s,
-                                             uint8_t* sm, int* taken, int limit, uint32_t q_full, int lane) {
+__device__ __forceinline__ void load_queries(const PagedArgs& a, const RowPiece& p, const SeqRows& s, uint8_t* sm,
+                                             int w, int warps, uint32_t q_full, int lane) {
   const int row0 = p.rb * C::M, rows = min(C::MS, s.n * a.hpr - row0), dq = C::D_H + a.d_r;
   const float* base = a.q_abs + ((long long)s.r0 * a.H + p.g * a.hpr) * dq;
   const long long token = (long long)a.H * dq;
-  for (;;) {
-    int t = 0;
-    if (lane == 0) {
-      t = *reinterpret_cast<volatile int*>(taken);
-      while (t < limit) {
-        const int was = atomicCAS(taken, t, t + 1);
-        if (was == t) break;
-        t = was;
-      }
-    }
-    t = __shfl_sync(0xffffffffu, t, 0);
-    if (t >= limit) break;
-    const int first = (t - (limit - C::GROUPS)) * C::GR;
-    load_query_part<C, C::D_H / 8, C::QSTEPS>(base, rows, first, row0, a.hpr, token, dq, sm, C::QB, false, C::D_H, lane);
-    if constexpr (C::DRP > 0)
-      load_query_part<C, C::DRP / 8, (C::GR * (C::DRP / 8) + 31) / 32>(base + C::D_H, rows, first, row0, a.hpr, token, dq,
-                                                                sm + C::OFF_QR, C::QRB, true, a.d_r, lane);
+  QueryGroup<C> now, next;
+  if (w < C::GROUPS) now.load(base, rows, w * 8, row0, a.hpr, token, dq, a.d_r, lane);
+  for (int t = w; t < C::GROUPS; t += warps) {
+    if (t + warps < C::GROUPS) next.load(base, rows, (t + warps) * 8, row0, a.hpr, token, dq, a.d_r, lane);
+    now.store(sm, t * 8, lane);
     fence_proxy_async_smem();   // the queries are read by the tensor core (async proxy)
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
+    now = next;
   }
 }
 // Ask L2 for the queries of a piece that is loaded later.
@@ -229,7 +231,6 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   long long* wtmp = reinterpret_cast<long long*>(
       (reinterpret_cast<uintptr_t>(prefix + 2 * a.B + 1) + 15) & ~uintptr_t(15));
   int* units = prefix + a.B + 1;
-  __shared__ int taken;   // query row groups taken so far
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hpr = a.hpr;
   if (threadIdx.x == 0) {
@@ -246,7 +247,6 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     mbar_init(q_full, C::GROUPS);
     mbar_init(q_free, 1);
     mbar_init(fin, 1);
-    taken = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   }
   if (threadIdx.x == 0) {
     if (total >= (1ll << 31)) atomicOr(a.status, GVA_DEVERR_RANGE);
-    a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();   // the prefix was read where TMA writes the ring
   tc::fence_before();
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       for (; more; more = walk.next()) {
         const int nk = p.k1 - p.k0, end = p.k1 * per_tile;
         if (lane == 0 && p.k0 == 0 && nk < p.nt)   // started here, ended elsewhere: where its pieces are
-          a.meta[blockIdx.x] = make_int4(ts.cta_of(walk.u + p.nt - 1) - (int)blockIdx.x + 1, p.b, p.g, p.rb);
+          write_row_meta(a, ts.cta_of(walk.u + p.nt - 1) - (int)blockIdx.x + 1, p, s, C::M);
         const int* row = a.table + (long long)p.b * a.table_stride;
         int base = p.k0 * per_tile;
         auto look = [&](int i) { return i < end ? slot_of(a, row, i << a.box_log2, s.L) : a.num_slots; };
@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           ok = ok && mbar_wait(q_free, (i - 1) & 1, a.status);
           ok = __all_sync(0xffffffffu, ok);
         }
-        load_queries<C>(a, p, s, sm, &taken, (i + 1) * C::GROUPS, q_full, lane);
+        // the softmax warps have nothing else to do before the first piece
+        load_queries<C>(a, p, s, sm, warp - 2, i > 0 ? 2 : 2 + 4 * C::NH, q_full, lane);
       }
     }
   } else {
@@ -426,9 +427,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     // A row of scores takes most of the registers: the walk waits in shared memory.
     __shared__ SoftmaxPiece pieces[4 * C::NH];
     SoftmaxPiece& sp = pieces[warp - 4];
-    int q_limit = C::GROUPS;
     if (more) {
-      load_queries<C>(a, p, s, sm, &taken, q_limit, q_full, lane);
+      load_queries<C>(a, p, s, sm, warp - 2, 2 + 4 * C::NH, q_full, lane);
       if (lane == 0) sp = SoftmaxPiece{walk.p, walk.s, walk.u, walk.end};
     }
     __syncwarp();
@@ -610,8 +610,6 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       }
       __syncwarp();
       more = sp.more;
-      q_limit += C::GROUPS;
-      if (more) load_queries<C>(a, sp.p, sp.s, sm, &taken, q_limit, q_full, lane);
       tc::fence_before();   // O has been read: the P of the next piece orders its first P.V behind
     }
   }
