@@ -99,10 +99,12 @@ __device__ __forceinline__ int slot_of(const PagedArgs& a, const int* row, int t
 // Row blocks.  The n * H/G query rows (token x head) of a value group of a sequence
 // are cut into blocks of M; block rb sees keys [0, kv_end) and takes
 // nt = max(1, ceil(kv_end / TK)) tiles (one masked tile where it sees none, which
-// yields its zeros).  A unit is one tile of one block; units are numbered by
-// sequence, block, group, tile, and CTA i takes units [i, i+1) * NT / grid: every CTA
-// gets the same number of tiles whatever the lengths, and a block whose units fall
-// to several CTAs is merged from their pieces.
+// yields its zeros).  Besides, a piece of a block costs about OV tiles (queries in,
+// outputs out), so a block counts as OV + nt units, its tiles the last nt of them: with
+// tiles alone, a CTA whose share was many short blocks ran 1.5 times as long as the rest.
+// Units are numbered by sequence, block and group, and CTA i takes units
+// [i, i+1) * NT / grid; a block whose tiles fall to several CTAs is merged from their
+// pieces.
 // ---------------------------------------------------------------------------
 // Sum over i in [0, n) of floor((a i + b) / m), all >= 0 (the Euclidean recursion on
 // the lattice points under a line).
@@ -128,7 +130,7 @@ __device__ inline unsigned long long floor_sum(U n, U m, U a, U b) {
   }
 }
 
-template <int M, int TK>
+template <int M, int TK, int OV>
 struct RowBlocks {
   const PagedArgs& a;
   __device__ __forceinline__ int blocks(const SeqRows& s) const {
@@ -155,7 +157,7 @@ struct RowBlocks {
                ? (long long)floor_sum<unsigned>(nb - 1, (unsigned)(h * TK), M, (unsigned)b)
                : (long long)floor_sum<unsigned long long>(nb - 1, h * TK, M, b);
     }
-    return u * a.G;
+    return (u + (long long)OV * nb) * a.G;
   }
   __device__ long long units(int b) const { return units(seq_rows(a, b)); }
 };
@@ -167,34 +169,34 @@ struct RowPiece {
 
 // The pieces of a CTA's units [u, end), in order.  first() is called by whole warps,
 // next() by any thread that called first().
-template <int M, int TK>
+template <int M, int TK, int OV>
 struct RowWalk {
-  RowBlocks<M, TK> rb;
+  RowBlocks<M, TK, OV> rb;
   const int* prefix;   // units before each sequence [B + 1], read by first() only
-  int u, end;
+  int u, end;          // first unit of the piece's block; end of the CTA's units
   RowPiece p;
   SeqRows s;
   // first piece; false if the CTA has none
-  __device__ bool first() {
-    if (u >= end) return false;
-    p.b = seq_at(prefix, rb.a.B, u);
+  __device__ bool first(int from) {
+    if (from >= end) return false;
+    p.b = seq_at(prefix, rb.a.B, from);
     s = seq_rows(rb.a, p.b);
-    return seek(u - prefix[p.b]);
+    return seek(from, from - prefix[p.b]);
   }
   // the same from one warp's batch
-  __device__ bool first(const LaneBatch& t) {
-    if (u >= end) return false;
-    const unsigned over = __ballot_sync(0xffffffffu, t.before + t.units > u);
+  __device__ bool first(int from, const LaneBatch& t) {
+    if (from >= end) return false;
+    const unsigned over = __ballot_sync(0xffffffffu, t.before + t.units > from);
     p.b = __ffs(over) - 1;
     s = shfl_rows(t.s, p.b);
-    return seek(u - __shfl_sync(0xffffffffu, t.before, p.b));
+    return seek(from, from - __shfl_sync(0xffffffffu, t.before, p.b));
   }
-  __device__ bool seek(int rem) {
-    // the block that holds unit u: lanes take consecutive blocks
+  __device__ bool seek(int from, int rem) {
+    // the block that holds unit `from`: lanes take consecutive blocks
     const int nb = rb.blocks(s), lane = threadIdx.x & 31;
     for (int base = 0;; base += 32) {
       const int i = base + lane;
-      const int mine = i < nb ? rb.a.G * rb.tiles(s, i) : 0;
+      const int mine = i < nb ? rb.a.G * (rb.tiles(s, i) + OV) : 0;
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -211,14 +213,19 @@ struct RowWalk {
       rem -= __shfl_sync(0xffffffffu, incl, 31);
     }
     p.nt = rb.tiles(s, p.rb);
-    p.g = (unsigned)rem / (unsigned)p.nt;
-    p.k0 = rem - p.g * p.nt;
-    clip();
-    return true;
+    p.g = (unsigned)rem / (unsigned)(p.nt + OV);
+    rem -= p.g * (p.nt + OV);
+    u = from - rem;
+    p.k0 = max(0, rem - OV);
+    return clip();
   }
-  __device__ __forceinline__ void clip() { p.k1 = min(p.nt, p.k0 + (end - u)); }
+  // tiles of the block before the CTA's end; none where that lies in its overhead
+  __device__ __forceinline__ bool clip() {
+    p.k1 = min(p.nt, end - u - OV);
+    return p.k1 > p.k0;
+  }
   __device__ bool next() {
-    u += p.k1 - p.k0;
+    u += OV + p.nt;
     if (u >= end) return false;
     p.k0 = 0;
     if (++p.g == rb.a.G) {
@@ -229,17 +236,20 @@ struct RowWalk {
       }
       p.nt = rb.tiles(s, p.rb);
     }
-    clip();
-    return true;
+    return clip();
   }
 };
 
-// Record of a block that this CTA starts and does not end: the number of its pieces,
-// and its rows (q row of its sequence, query rows of the block).
-__device__ __forceinline__ void write_row_meta(const PagedArgs& a, int pieces, const RowPiece& p,
-                                               const SeqRows& s, int M) {
+// Record of a block that this CTA starts and does not end: the number of its pieces (up
+// to the CTA of its last tile), and its rows (q row of its sequence, query rows of it).
+template <int M, int TK, int OV>
+__device__ __forceinline__ void write_row_meta(const PagedArgs& a, const TileSplit& ts,
+                                               const RowWalk<M, TK, OV>& w) {
+  const RowPiece& p = w.p;
+  if (p.k0 > 0 || p.k1 == p.nt) return;
+  const int pieces = ts.cta_of(w.u + OV + p.nt - 1) - (int)blockIdx.x + 1;
   a.meta[2 * blockIdx.x] = make_int4(pieces, p.b, p.g, p.rb);
-  a.meta[2 * blockIdx.x + 1] = make_int4(s.r0, s.n * a.hpr - p.rb * M, 0, 0);
+  a.meta[2 * blockIdx.x + 1] = make_int4(w.s.r0, w.s.n * a.hpr - p.rb * M, 0, 0);
 }
 
 // Where a piece's partial state goes: a CTA leaves at most one block that it did not

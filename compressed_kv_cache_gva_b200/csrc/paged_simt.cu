@@ -16,7 +16,7 @@ namespace gva {
 
 namespace {
 
-constexpr int kM = kPagedSimtRows, kTK = 32, kThreads = 256;
+constexpr int kM = kPagedSimtRows, kTK = 32, kOV = 1, kThreads = 256;
 constexpr int kMaxD = 512;
 
 struct SimtSmem {
@@ -59,18 +59,17 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
   // queries, lengths, tables and cache rows may come from the kernels before
   pdl_enter(a);
   if (blockIdx.x == 0 && a.flag_errors) flag_bad_sequences(a);
-  const RowBlocks<kM, kTK> blocks{a};
+  const RowBlocks<kM, kTK, kOV> blocks{a};
   TileSplit ts;
   long long total;
-  RowWalk<kM, kTK> walk{blocks, prefix, 0, 0, {}, {}};
+  RowWalk<kM, kTK, kOV> walk{blocks, prefix, 0, 0, {}, {}};
   if (a.B <= kLaneBatch) {
     const LaneBatch t = lane_batch(a, [&](const SeqRows& s) { return blocks.units(s); });
     total = t.total;
     ts = make_split(total < (1ll << 31) ? (int)total : 0, (int)gridDim.x, 0);
-    walk.u = ts.first(blockIdx.x);
     walk.end = ts.first(blockIdx.x + 1);
     if (tid < 32) {
-      const bool any = walk.first(t);
+      const bool any = walk.first(ts.first(blockIdx.x), t);
       if (tid == 0) {
         more = any;
         piece = walk.p;
@@ -79,10 +78,9 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
   } else {
     total = block_scan(a.B, [&](int b) { return blocks.units(b); }, prefix, wtmp);
     ts = make_split(prefix[a.B], (int)gridDim.x, 0);
-    walk.u = ts.first(blockIdx.x);
     walk.end = ts.first(blockIdx.x + 1);
     if (tid < 32) {
-      const bool any = walk.first();
+      const bool any = walk.first(ts.first(blockIdx.x));
       if (tid == 0) {
         more = any;
         piece = walk.p;
@@ -182,10 +180,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
       }
     }
     if (tid == 0) {
-      if (p.k0 == 0 && !whole) {
-        const int start = walk.u;   // the block's first unit, and the CTA that ends it
-        write_row_meta(a, ts.cta_of(start + p.nt - 1) - (int)blockIdx.x + 1, p, s, kM);
-      }
+      write_row_meta(a, ts, walk);
       more = walk.next();
       piece = walk.p;
     }

@@ -32,6 +32,10 @@ namespace gva {
 
 namespace {
 
+#ifndef GVA_TC_OV
+#define GVA_TC_OV 3
+#endif
+
 template <int D_H_, int DRP_, bool HILO_, int MS_>
 struct PtCfg {
   static constexpr int D_H = D_H_, DRP = DRP_;
@@ -54,6 +58,7 @@ struct PtCfg {
   // an SM one each does as well and costs no exchange (d_h = 64 chunk 168 against 174 us).
   static constexpr int NH = D_H == 64 ? 1 : 2;
   static constexpr int HK = TK / NH, HD = D_H / NH;   // keys and output columns of a softmax warp
+  static constexpr int OV = GVA_TC_OV;       // cost of a piece, in tiles
   static constexpr int CB = D_H / 64, KS = D_H / 16, RS = DRP / 16;
   static constexpr int QB = MS * D_H * 2;    // q~ hi (or lo): CB blocks of MS rows x 128 B
   static constexpr int GROUPS = MS / 8;      // of query rows, as loaded
@@ -260,9 +265,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   // queries, lengths, tables and cache rows may come from the kernels before
   pdl_enter(a);
   if (blockIdx.x == 0 && a.flag_errors) flag_bad_sequences(a);
-  const RowBlocks<C::M, C::TK> blocks{a};
+  const RowBlocks<C::M, C::TK, C::OV> blocks{a};
   // Every role walks the CTA's pieces by itself.
-  RowWalk<C::M, C::TK> walk{blocks, prefix, 0, 0, {}, {}};
+  RowWalk<C::M, C::TK, C::OV> walk{blocks, prefix, 0, 0, {}, {}};
   TileSplit ts;
   long long total;
   bool more;
@@ -270,18 +275,16 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     const LaneBatch t = lane_batch(a, [&](const SeqRows& s) { return blocks.units(s); });
     total = t.total;
     ts = make_split(total < (1ll << 31) ? (int)total : 0, (int)gridDim.x, 0);
-    walk.u = ts.first(blockIdx.x);
     walk.end = ts.first(blockIdx.x + 1);
-    more = walk.first(t);
+    more = walk.first(ts.first(blockIdx.x), t);
   } else {
     const int per = (a.B + C::THREADS - 1) / C::THREADS;   // as block_scan deals them out
     for (int b = threadIdx.x * per; b < min((int)(threadIdx.x + 1) * per, a.B); ++b)
       units[b] = (int)min(blocks.units(b), 0x7fffffffll);
     total = block_scan(a.B, [&](int b) { return (long long)units[b]; }, prefix, wtmp);
     ts = make_split(prefix[a.B], (int)gridDim.x, 0);
-    walk.u = ts.first(blockIdx.x);
     walk.end = ts.first(blockIdx.x + 1);
-    more = walk.first();
+    more = walk.first(ts.first(blockIdx.x));
   }
   if (threadIdx.x == 0) {
     if (total >= (1ll << 31)) atomicOr(a.status, GVA_DEVERR_RANGE);
@@ -307,8 +310,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       const int per_tile = C::TK >> a.box_log2;
       for (; more; more = walk.next()) {
         const int nk = p.k1 - p.k0, end = p.k1 * per_tile;
-        if (lane == 0 && p.k0 == 0 && nk < p.nt)   // started here, ended elsewhere: where its pieces are
-          write_row_meta(a, ts.cta_of(walk.u + p.nt - 1) - (int)blockIdx.x + 1, p, s, C::M);
+        if (lane == 0) write_row_meta(a, ts, walk);
         const int* row = a.table + (long long)p.b * a.table_stride;
         int base = p.k0 * per_tile;
         auto look = [&](int i) { return i < end ? slot_of(a, row, i << a.box_log2, s.L) : a.num_slots; };
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       kt += nk;
       __syncwarp();
       if (lane == 0) {
-        RowWalk<C::M, C::TK> w{blocks, nullptr, sp.u, sp.end, sp.p, sp.s};
+        RowWalk<C::M, C::TK, C::OV> w{blocks, nullptr, sp.u, sp.end, sp.p, sp.s};
         sp.more = w.next();
         sp.p = w.p;
         sp.s = w.s;
