@@ -32,9 +32,6 @@ namespace gva {
 
 namespace {
 
-#ifndef GVA_TC_OV
-#define GVA_TC_OV 3
-#endif
 
 template <int D_H_, int DRP_, bool HILO_, int MS_>
 struct PtCfg {
@@ -58,10 +55,9 @@ struct PtCfg {
   // an SM one each does as well and costs no exchange (d_h = 64 chunk 168 against 174 us).
   static constexpr int NH = D_H == 64 ? 1 : 2;
   static constexpr int HK = TK / NH, HD = D_H / NH;   // keys and output columns of a softmax warp
-  static constexpr int OV = GVA_TC_OV;       // cost of a piece, in tiles
+  static constexpr int OV = D_H == 64 ? 3 : 4;   // cost of a piece, in tiles
   static constexpr int CB = D_H / 64, KS = D_H / 16, RS = DRP / 16;
   static constexpr int QB = MS * D_H * 2;    // q~ hi (or lo): CB blocks of MS rows x 128 B
-  static constexpr int GROUPS = MS / 8;      // of query rows, as loaded
   static constexpr int QRB = DRP ? (MS * DRP * 2 + 1023) / 1024 * 1024 : 0;
   static constexpr int VB = CB * TK * 128;
   static constexpr int KRB = DRP * TK * 2;
@@ -104,13 +100,14 @@ __device__ __forceinline__ uint32_t sw_pos(int r, int chunk) {
                    : (uint32_t)(r * 32 + ((chunk ^ ((r >> 2) & 1)) << 4));
 }
 
+// x = hi + lo in two bf16 each (pairs share a conversion: those queue behind the
+// exponentials of the softmax warps).
 __device__ __forceinline__ uint4 split_bf16(const float* x, uint4& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = x[2 * i], b = x[2 * i + 1], ah = bf16_round(a), bh = bf16_round(b);
-    h[i] = pack_bf16(ah, bh);
-    l[i] = pack_bf16(a - ah, b - bh);
+    h[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    l[i] = pack_bf16(x[2 * i] - __uint_as_float(h[i] << 16), x[2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
   }
   lo = make_uint4(l[0], l[1], l[2], l[3]);
   return make_uint4(h[0], h[1], h[2], h[3]);
@@ -131,73 +128,87 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Queries of a piece -> shared memory: bf16 hi and lo halves, swizzled K-major rows.
-// Warp w of `warps` takes groups w, w + warps, ... of GR = 8 rows, the loads of the next
-// group in flight while it splits and stores one (the latency of L2 is most of the time
-// of two warps).
-template <class C>
-struct QueryGroup {
-  static constexpr int W = C::D_H / 8, STEPS = 8 * W / 32, RW = C::DRP / 8;   // chunks of 8 elements of a row
-  float4 x[STEPS][2], y[2];
-  __device__ __forceinline__ void load(const float* base, int rows, int first, unsigned row0, unsigned hpr,
-                                       long long token, int dq, int d_r, int lane) {
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto row = [&](int r) {
-      const unsigned R = row0 + r, qi = R / hpr;
-      return base + qi * token + (R - qi * hpr) * dq;
-    };
-#pragma unroll
-    for (int u = 0; u < STEPS; ++u) {
-      const int r = first + u * (32 / W) + lane / W;
-      x[u][0] = x[u][1] = zero;
-      if (r < rows) {
-        const float* src = row(r) + (lane % W) * 8;
-        x[u][0] = *reinterpret_cast<const float4*>(src);
-        x[u][1] = *reinterpret_cast<const float4*>(src + 4);
+// Queries of a piece -> shared memory: bf16 hi and lo halves, swizzled K-major rows; by
+// threads tid of nthr.  A chunk of 8 fp32 elements takes the room of its two halves, so
+// its two 16-byte parts are first copied there raw, all of them in flight at once
+// (asynchronous copies hold no registers), and each thread then splits its own chunks in
+// place.  (Through registers, a group of rows at a time, two warps took 10 us for the
+// next piece's queries; a load's latency is ~1 us beside the stream.)
+template <class C, bool POS, int NTHR>
+struct QueryPart {
+  static constexpr int W = (POS ? C::DRP : C::D_H) / 8;   // chunks of a row
+  static constexpr int HALF = POS ? C::QRB : C::QB;       // from the hi to the lo half
+  static constexpr int STEP = NTHR / W, N = (C::MS + STEP - 1) / STEP;   // rows apart; rows of a thread at most
+  __device__ static __forceinline__ uint32_t at(int r, int c) {
+    return POS ? C::OFF_QR + sw_pos<C::DRP>(r, c) : (uint32_t)((c / 8) * (C::MS * 128)) + sw128(r, c % 8);
+  }
+  __device__ static __forceinline__ void copy(const float* base, int rows, unsigned row0, int hpr, long long token,
+                                              int dq, int width, uint32_t sb, int tid) {
+    const int c = tid % W, r0 = tid / W;
+    const unsigned R = row0 + r0;
+    int h = R % (unsigned)hpr;
+    const float* src = base + (R / (unsigned)hpr) * token + h * dq + c * 8;
+    const int dh = STEP % hpr;   // the next row of this thread: STEP rows on
+    const long long step = (STEP / hpr) * token + dh * dq, wrap = token - (long long)hpr * dq;
+#pragma unroll 2
+    for (int i = 0; i < N; ++i) {
+      const int r = r0 + i * STEP;
+      if (N * STEP == C::MS || r < C::MS) {
+        const bool on = r < rows && c * 8 < width;
+        const uint32_t dst = sb + at(r, c), n = on ? 16 : 0;   // 0: zeros, nothing is read
+        const float* from = on ? src : base;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + HALF), "l"(on ? src + 4 : base), "r"(n)
+                     : "memory");
       }
-    }
-    if constexpr (RW > 0) {
-      const int i = lane / RW, c = lane % RW;
-      y[0] = y[1] = zero;
-      if (i < 8 && first + i < rows && c * 8 < d_r) {
-        const float* src = row(first + i) + C::D_H + c * 8;
-        y[0] = *reinterpret_cast<const float4*>(src);
-        y[1] = *reinterpret_cast<const float4*>(src + 4);
+      src += step;
+      h += dh;
+      if (h >= hpr) {
+        h -= hpr;
+        src += wrap;
       }
     }
   }
-  __device__ __forceinline__ void store(uint8_t* sm, int first, int lane) const {
-    auto put = [&](const float4& a, const float4& b, uint8_t* dst, int half) {
-      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      uint4 lo;
-      *reinterpret_cast<uint4*>(dst) = split_bf16(v, lo);
-      *reinterpret_cast<uint4*>(dst + half) = lo;
-    };
+  __device__ static __forceinline__ void split(uint8_t* sm, int tid) {
+    const int c = tid % W, r0 = tid / W;
+    constexpr int U = N < 2 ? N : 2;   // chunks at once: their chains overlap
+#pragma unroll 1
+    for (int i = 0; i < N; i += U) {
+      float4 x[U], y[U];
 #pragma unroll
-    for (int u = 0; u < STEPS; ++u) {
-      const int r = first + u * (32 / W) + lane / W, c = lane % W;
-      put(x[u][0], x[u][1], sm + (c / 8) * (C::MS * 128) + sw128(r, c % 8), C::QB);
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + (i + u) * STEP;
+        if (r < C::MS) {
+          x[u] = *reinterpret_cast<const float4*>(sm + at(r, c));
+          y[u] = *reinterpret_cast<const float4*>(sm + at(r, c) + HALF);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + (i + u) * STEP;
+        if (r < C::MS) {
+          const float v[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
+          uint4 lo;
+          *reinterpret_cast<uint4*>(sm + at(r, c)) = split_bf16(v, lo);
+          *reinterpret_cast<uint4*>(sm + at(r, c) + HALF) = lo;
+        }
+      }
     }
-    if constexpr (RW > 0)
-      if (lane / RW < 8) put(y[0], y[1], sm + C::OFF_QR + sw_pos<C::DRP>(first + lane / RW, lane % RW), C::QRB);
   }
 };
-template <class C>
+template <class C, int NTHR>
 __device__ __forceinline__ void load_queries(const PagedArgs& a, const RowPiece& p, const SeqRows& s, uint8_t* sm,
-                                             int w, int warps, uint32_t q_full, int lane) {
+                                             int tid) {
   const int row0 = p.rb * C::M, rows = min(C::MS, s.n * a.hpr - row0), dq = C::D_H + a.d_r;
   const float* base = a.q_abs + ((long long)s.r0 * a.H + p.g * a.hpr) * dq;
   const long long token = (long long)a.H * dq;
-  QueryGroup<C> now, next;
-  if (w < C::GROUPS) now.load(base, rows, w * 8, row0, a.hpr, token, dq, a.d_r, lane);
-  for (int t = w; t < C::GROUPS; t += warps) {
-    if (t + warps < C::GROUPS) next.load(base, rows, (t + warps) * 8, row0, a.hpr, token, dq, a.d_r, lane);
-    now.store(sm, t * 8, lane);
-    fence_proxy_async_smem();   // the queries are read by the tensor core (async proxy)
-    __syncwarp();
-    if (lane == 0) mbar_arrive(q_full);
-    now = next;
-  }
+  QueryPart<C, false, NTHR>::copy(base, rows, row0, a.hpr, token, dq, C::D_H, smem_u32(sm), tid);
+  if constexpr (C::DRP > 0)
+    QueryPart<C, true, NTHR>::copy(base + C::D_H, rows, row0, a.hpr, token, dq, a.d_r, smem_u32(sm), tid);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  QueryPart<C, false, NTHR>::split(sm, tid);
+  if constexpr (C::DRP > 0) QueryPart<C, true, NTHR>::split(sm, tid);
+  fence_proxy_async_smem();   // the queries are read by the tensor core (async proxy)
 }
 // Ask L2 for the queries of a piece that is loaded later.
 template <class C>
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     }
     mbar_init(p_full, 4 * C::NH);
     mbar_init(pv_done, 1);
-    mbar_init(q_full, C::GROUPS);
+    mbar_init(q_full, 2);
     mbar_init(q_free, 1);
     mbar_init(fin, 1);
     fence_barrier_init();
@@ -415,8 +426,14 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           ok = ok && mbar_wait(q_free, (i - 1) & 1, a.status);
           ok = __all_sync(0xffffffffu, ok);
         }
-        // the softmax warps have nothing else to do before the first piece
-        load_queries<C>(a, p, s, sm, warp - 2, i > 0 ? 2 : 2 + 4 * C::NH, q_full, lane);
+        // the softmax warps have nothing else to do before the first piece, and help
+        if (i > 0) load_queries<C, 64>(a, p, s, sm, threadIdx.x - 64);
+        else {
+          load_queries<C, C::THREADS - 64>(a, p, s, sm, threadIdx.x - 64);
+          named_bar_sync(5, C::THREADS - 64);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
       }
     }
   } else {
@@ -430,7 +447,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     __shared__ SoftmaxPiece pieces[4 * C::NH];
     SoftmaxPiece& sp = pieces[warp - 4];
     if (more) {
-      load_queries<C>(a, p, s, sm, warp - 2, 2 + 4 * C::NH, q_full, lane);
+      load_queries<C, C::THREADS - 64>(a, p, s, sm, threadIdx.x - 64);
+      named_bar_sync(5, C::THREADS - 64);
       if (lane == 0) sp = SoftmaxPiece{walk.p, walk.s, walk.u, walk.end};
     }
     __syncwarp();
@@ -492,13 +510,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
               float2 e = add2(make_float2(x[16 * q + 2 * i], x[16 * q + 2 * i + 1]), neg);
               e = make_float2(ex2(e.x), ex2(e.y));
               sum[i & 3] = add2(sum[i & 3], e);
-              if constexpr (C::HILO) {
-                const float hx = bf16_round(e.x), hy = bf16_round(e.y);
-                hi[i] = pack_bf16(hx, hy);
-                lo[i] = pack_bf16(e.x - hx, e.y - hy);
-              } else {
-                hi[i] = pack_bf16(e.x, e.y);
-              }
+              hi[i] = pack_bf16(e.x, e.y);
+              if constexpr (C::HILO)
+                lo[i] = pack_bf16(e.x - __uint_as_float(hi[i] << 16), e.y - __uint_as_float(hi[i] & 0xffff0000u));
             }
             if (q == 0 && kk >= 1) {   // P is free, and O still, once the P.V before has completed
               ok = ok && mbar_wait(pv_done, (kk - 1) & 1, a.status);
