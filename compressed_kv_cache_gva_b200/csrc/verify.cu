@@ -13,7 +13,7 @@
 //
 // What bounds it: memory.  Besides k probabilities a request reads one row of each
 // model, vocab * 2 * 4 bytes, once.  A cluster of CTAs shares a request: each warp
-// sums a contiguous chunk (16-byte loads, two in flight per row and lane, four CTAs per SM), the
+// sums a contiguous chunk through a ring in shared memory, four CTAs per SM, the
 // chunk sums meet through distributed shared memory, and the CTA whose chunk
 // holds the answer reads it again from L2, an eighth per warp.
 // Sums are in 64 bits: with ~10^5 tokens of mass ~10^-5 each, 32-bit running sums
@@ -30,7 +30,9 @@ namespace {
 constexpr int kVfWarps = 8;
 constexpr int kVfThreads = 32 * kVfWarps;
 constexpr int kVfMaxCluster = 8;
-constexpr int kVfUnroll = 2;   // 16-byte vectors in flight per lane and row
+// A warp's part of the shared-memory ring: units of 512 bytes (a 16-byte vector per lane).
+constexpr int kVfUnits = 12;
+constexpr int kVfRing = kVfWarps * kVfUnits * 512;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -113,29 +115,76 @@ __device__ __forceinline__ double warp_sum(double x) {
   return x;
 }
 
+// Exact sum of two floats: their rounded sum, and what the rounding left (Knuth's TwoSum).
+__device__ __forceinline__ float two_sum(float a, float b, float& err) {
+  const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
+  err = __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z));
+  return s;
+}
+
 // Sum of the chunk's weights: lanes take vectors 32 apart.
+// A 64-bit weight per element costs two conversions at 16 a clock and SM, which took
+// longer than the memory (64 requests x 131072 tokens: 24.5 us).  So a weight is kept as
+// its rounded float and the rounding's exact error (p - q with p > q: Dekker's), pairs are
+// added the same way, one value per pair goes to the 64-bit sum, and the errors, 2^-24 of
+// the values, are summed in 32 bits (2^-48 of the values).
+//
+// The vectors pass through the warp's ring by asynchronous copies, 12 of a row (6 of
+// each of two) in flight per lane: four in registers left a warp waiting one DRAM latency
+// per 1 KB, 10 of 24 us at that size.  A lane reads only what it copied itself, so nothing
+// is synchronised.  Vectors that are not aligned or leave the row go through registers.
 template <typename T>
-__device__ __forceinline__ double chunk_sum(const Weights<T>& W, int v0, int v1, int lane) {
-  constexpr int N = RowVec<T>::N, SEG = 32 * N;
-  double acc = 0.0;
-  for (int s = v0; s < v1; s += kVfUnroll * SEG) {
-    uint4 up[kVfUnroll], uq[kVfUnroll];
-#pragma unroll
-    for (int u = 0; u < kVfUnroll; ++u) {
-      const int v = s + u * SEG + lane * N;
-      const bool on = s + u * SEG < v1;
-      up[u] = on ? W.load_p(v) : make_uint4(0, 0, 0, 0);
-      uq[u] = on ? W.load_q(v) : make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void fetch(const T* row, int v, int n, bool vec, uint32_t dst, uint8_t* at) {
+  if (vec && v >= 0 && v + RowVec<T>::N <= n)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row + v) : "memory");
+  else
+    *reinterpret_cast<uint4*>(at) = load_vec(row, v, n, false);
+}
+template <typename T, bool Q>
+__device__ __forceinline__ double chunk_sum_of(const Weights<T>& W, int v0, int v1, uint8_t* ring, int lane) {
+  constexpr int N = RowVec<T>::N, SEG = 32 * N, S = Q ? kVfUnits / 2 : kVfUnits;
+  ring += lane * 16;
+  const uint32_t base = smem_u32(ring);
+  auto issue = [&](int i) {
+    const int v = v0 + i * SEG + lane * N, slot = i % S * (Q ? 1024 : 512);
+    if (v0 + i * SEG < v1) {
+      fetch(W.p, v, W.vocab, true, base + slot, ring + slot);
+      if constexpr (Q) fetch(W.q, v, W.vocab, W.vec_q, base + slot + 512, ring + slot + 512);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = 0; i < S - 1; ++i) issue(i);
+  double acc = 0.0;
+  float rest = 0.f;
+  for (int i = 0; v0 + i * SEG < v1; ++i) {
+    issue(i + S - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    const int v = v0 + i * SEG + lane * N, slot = i % S * (Q ? 1024 : 512);
+    float p[N], q[N];
+    widen(*reinterpret_cast<const uint4*>(ring + slot), p);
+    if constexpr (Q) widen(*reinterpret_cast<const uint4*>(ring + slot + 512), q);
 #pragma unroll
-    for (int u = 0; u < kVfUnroll; ++u) {
-      double w[N];
-      W.get(s + u * SEG + lane * N, up[u], uq[u], w);
+    for (int j = 0; j < N; j += 2) {
+      float d[2], e[2], t;
 #pragma unroll
-      for (int i = 0; i < N; i += 2) acc += w[i] + w[i + 1];
+      for (int u = 0; u < 2; ++u) {
+        const float x = p[j + u], y = Q ? q[j + u] : 0.f;
+        const float r = __fsub_rn(x, y);
+        const bool on = r > 0.f && v + j + u != W.skip;
+        d[u] = on ? r : 0.f;
+        // a draft's probability is >= 0, so x >= y here and this is exact
+        e[u] = Q && on ? __fsub_rn(__fsub_rn(x, r), y) : 0.f;
+      }
+      acc += (double)two_sum(d[0], d[1], t);
+      rest += t + (e[0] + e[1]);
     }
   }
-  return warp_sum(acc);
+  asm volatile("cp.async.wait_all;" ::: "memory");   // the ring is free again
+  return warp_sum(acc + (double)rest);
+}
+template <typename T>
+__device__ __forceinline__ double chunk_sum(const Weights<T>& W, int v0, int v1, uint8_t* ring, int lane) {
+  return W.q ? chunk_sum_of<T, true>(W, v0, v1, ring, lane) : chunk_sum_of<T, false>(W, v0, v1, ring, lane);
 }
 
 // First v of the chunk whose running sum (from `base`) exceeds t; the last v with a
@@ -186,7 +235,9 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
   __shared__ double sums[kVfWarps];
   __shared__ double all[kVfMaxCluster * kVfWarps];
   __shared__ int s_first;
+  extern __shared__ __align__(16) uint8_t vf_ring[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t* ring = vf_ring + warp * kVfUnits * 512;
   const int b = (int)blockIdx.x / cl;
   const uint32_t rank = cl > 1 ? cluster_rank() : 0u;
   // probabilities and tokens come from the kernels before
@@ -245,7 +296,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
   bool found = false;
   for (int pass = 0; pass < 2; ++pass) {
     const int c = (int)rank * kVfWarps + warp;
-    const double s = chunk_sum(W, edge(c), edge(c + 1), lane);
+    const double s = chunk_sum(W, edge(c), edge(c + 1), ring, lane);
     if (lane == 0) sums[warp] = s;
     __syncthreads();
     if (cl > 1) {
@@ -291,7 +342,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
         // then the one warp whose eighth holds the answer walks it
         const int v0 = edge(ch), sub = (len / kVfWarps + SEG - 1) / SEG * SEG, v1 = edge(ch + 1);
         const int w0 = min(v0 + warp * sub, v1), w1 = min(v0 + (warp + 1) * sub, v1);
-        const double sw = chunk_sum(W, w0, w1, lane);
+        const double sw = chunk_sum(W, w0, w1, ring, lane);
         if (lane == 0) sums[warp] = sw;
         __syncthreads();
         int at = -1, last = -1;
@@ -342,8 +393,11 @@ cudaError_t launch_verify(const VerifyArgs& a, bool bf16, int num_sms, cudaStrea
   while (cl > 1 && (long long)a.B * cl > 4ll * num_sms) cl >>= 1;   // one wave of CTAs
   static_assert(kVfMaxCluster * kVfWarps <= 64, "two chunk sums per lane");
   const dim3 grid((unsigned)(a.B * cl)), block(kVfThreads);
-  if (bf16) return launch_pdl_cluster(verify_kernel<__nv_bfloat16>, grid, block, cl, 0, st, a, cl);
-  return launch_pdl_cluster(verify_kernel<float>, grid, block, cl, 0, st, a, cl);
+  auto go = [&](auto k) {
+    const cudaError_t e = ensure_max_smem(k, kVfRing);
+    return e == cudaSuccess ? launch_pdl_cluster(k, grid, block, cl, kVfRing, st, a, cl) : e;
+  };
+  return bf16 ? go(verify_kernel<__nv_bfloat16>) : go(verify_kernel<float>);
 }
 
 }  // namespace gva
