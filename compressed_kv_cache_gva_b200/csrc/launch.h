@@ -56,7 +56,8 @@ cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, 
   return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
 }
 
-// Same, as clusters of `cl` thread blocks along x (1 <= cl <= 8, dividing grid.x).
+// Same, as clusters of `cl` thread blocks along x (dividing grid.x; more than 8 need the
+// kernel's opt-in).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl_cluster(void (*k)(KArgs...), dim3 grid, dim3 block, int cl, size_t smem,
                                cudaStream_t st, Args&&... args) {

@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kPlanMaxThreads = 1024;
 constexpr int kPlanPer = kMaxBatch / kPlanMaxThreads;   // requests per thread at most
+constexpr int kPlanCluster = 16;                        // CTAs of a large step
 constexpr int kTok = 4;                                 // new tokens per thread in flight
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -258,10 +259,19 @@ cudaError_t launch_plan_pages(const PlanArgs& a, cudaStream_t st) {
   int threads = 128;
   while (threads < kPlanMaxThreads && threads * 4 < max(a.B * 4, a.max_new)) threads *= 2;
   if (threads * kPlanPer < a.B) threads = kPlanMaxThreads;
-  const int cl = (a.B > 512 || a.max_new > 4096) ? 8 : 1;
+  // One CTA for small steps; else a cluster of 16 (the most there is, opt-in): the step
+  // of 2048 requests and 39102 new tokens takes 13.4 us with 16 CTAs, 15.8 with 8.
+  const int cl = (a.B > 512 || a.max_new > 4096) ? kPlanCluster : 1;
   const size_t smem = sizeof(int) * (size_t)(6 * a.B + 3);
   cudaError_t e = ensure_max_smem(plan_pages_kernel, smem);
   if (e != cudaSuccess) return e;
+  const void* key = reinterpret_cast<const void*>(plan_pages_kernel);
+  const int wide = (int)cudaFuncAttributeNonPortableClusterSizeAllowed;
+  if (cl > 8 && !attr_applied(key, wide, 1)) {
+    e = cudaFuncSetAttribute(plan_pages_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    attr_record(key, wide, 1);
+  }
   return launch_pdl_cluster(plan_pages_kernel, dim3(cl), dim3(threads), cl, smem, st, a, cl);
 }
 

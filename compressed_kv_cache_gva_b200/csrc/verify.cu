@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
 
 cudaError_t launch_verify(const VerifyArgs& a, bool bf16, int num_sms, cudaStream_t st) {
   int cl = kVfMaxCluster;
-  while (cl > 1 && (long long)a.B * cl > 4ll * num_sms) cl >>= 1;   // one wave of CTAs
+  while (cl > 1 && (long long)a.B * cl > 3ll * num_sms) cl >>= 1;   // (3: 21.4, 4: 22.8 us, 256 requests)
   static_assert(kVfMaxCluster * kVfWarps <= 64, "two chunk sums per lane");
   const dim3 grid((unsigned)(a.B * cl)), block(kVfThreads);
   auto go = [&](auto k) {
