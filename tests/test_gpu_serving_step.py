@@ -54,7 +54,8 @@ class Server:
                          self.acc, self.seq_len, self.kept, self.err)
 
     def draw(self, n_new):
-        """New tokens' values, keys and queries, and the models' probabilities, for this step."""
+        """New tokens' values, keys and queries, and the models' probabilities, for this step.
+        Steps with a prompt keep all of their tokens (random numbers 0 accept every draft)."""
         g, r = self.g, self.room
         rnd = lambda t: t.copy_(torch.randn(t.shape, generator=g))
         for t in (self.q, self.v, self.kpe):
@@ -66,7 +67,7 @@ class Server:
         tok = torch.randint(0, VOCAB, (r,), generator=g)
         tok[1:] = torch.multinomial(dr, 1, generator=g)[:-1, 0]
         self.tokens.copy_(tok)
-        self.u.copy_(torch.rand(r, generator=g))
+        self.u.copy_(torch.rand(r, generator=g) * (max(n_new) <= 8))
         self.us.copy_(torch.rand(self.B, generator=g))
         self.n_new.copy_(torch.tensor(n_new, dtype=I32))
         self.out.fill_(3.25)
