@@ -500,10 +500,13 @@ gva_status_t gva_plan_pages(int32_t B, int32_t page_size, int32_t num_pages, int
  *   workspace  zeroed once; gva_paged_workspace_size bytes; its first word is the
  *              status word (GVA_DEVERR_*), as for gva_decode_attention.  Calls that may
  *              overlap on the GPU (streams, or graphs) must use different workspaces.
- * Slots behind a request's end may hold anything, NaN included.  On the device: a page
- * id outside the cache, or a request longer than its table row, reads as 0 there and
- * sets GVA_DEVERR_RANGE; a request whose row range is negative, leaves [0, n_rows) or
- * exceeds max_query_len, or whose length is negative, is skipped and sets it too.
+ * Slots behind a request's end may hold anything, NaN included.  The request's own cached
+ * tokens are finite: a NaN or infinity in one of them may reach every new token of the
+ * request, those before it too (their probability of it is 0, and 0 x NaN is NaN).
+ * On the device: a page id outside the cache, or a request longer than its table row,
+ * reads as 0 there and sets GVA_DEVERR_RANGE; a request whose row range is negative,
+ * leaves [0, n_rows) or exceeds max_query_len, or whose length is negative or above
+ * num_slots, is skipped and sets it too.
  *
  * Three kernels share the batch by new tokens per request:
  *  - up to 8 query columns (new tokens * H/G) per value group: split-KV over all SMs on

@@ -221,9 +221,10 @@ def test_inconsistent_row_ranges_are_skipped():
         for b in range(3):
             ref[b][r0:r1] = np.nan
         keep = x.q_start.copy()
-        on = x.device()
-        on["L"][1] = -3                                       # a negative length
-        x.check(x.run(flags=flags, status=gva.DEVERR_RANGE, on=on), ref, F32, 2.0 ** -16)
+        for length in (-3, x.num_pages * x.page + 1, 2 ** 31 - 1):   # negative; above all slots
+            on = x.device()
+            on["L"][1] = length
+            x.check(x.run(flags=flags, status=gva.DEVERR_RANGE, on=on), ref, F32, 2.0 ** -16)
         on = x.device()
         on["q_start"][3] = x.rows + 1                         # leaves the buffers
         ref2 = x.reference()
