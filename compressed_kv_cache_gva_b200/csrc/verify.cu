@@ -233,7 +233,7 @@ __device__ __forceinline__ int chunk_find(const Weights<T>& W, int v0, int v1, d
 
 template <typename T>
 __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs a, const int cl) {
-  __shared__ double sums[kVfWarps];
+  __shared__ double sums[kVfWarps], part[kVfWarps];
   __shared__ double all[kVfMaxCluster * kVfWarps];
   __shared__ int s_first;
   extern __shared__ __align__(16) uint8_t vf_ring[];
@@ -307,10 +307,8 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
     for (int i = tid; i < chunks; i += kVfThreads)
       all[i] = cl > 1 ? ld_cluster_f64(&sums[i % kVfWarps], i / kVfWarps) : sums[i];
     __syncthreads();
-    if (cl > 1) {   // remote reads done: the sums may change, and CTAs may leave
-      cl_arrive();
-      cl_wait();
-    }
+    // remote reads done; waited for before the sums change or a CTA leaves
+    if (cl > 1) cl_arrive();
     // every warp finds the chunk by itself: lanes hold consecutive pairs of chunk sums
     const double s0 = 2 * lane < chunks ? all[2 * lane] : 0.0;
     const double s1 = 2 * lane + 1 < chunks ? all[2 * lane + 1] : 0.0;
@@ -344,12 +342,12 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
         const int v0 = edge(ch), sub = (len / kVfWarps + SEG - 1) / SEG * SEG, v1 = edge(ch + 1);
         const int w0 = min(v0 + warp * sub, v1), w1 = min(v0 + (warp + 1) * sub, v1);
         const double sw = chunk_sum(W, w0, w1, ring, lane);
-        if (lane == 0) sums[warp] = sw;
+        if (lane == 0) part[warp] = sw;
         __syncthreads();
         int at = -1, last = -1;
         double run = base, from = base;
         for (int w = 0; w < kVfWarps; ++w) {
-          const double x = sums[w];
+          const double x = part[w];
           if (x > 0.0) {
             last = w;
             if (at < 0) {
@@ -374,6 +372,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
     // the residual is empty (p <= q everywhere): draw from p itself
     W.q = nullptr;
     W.skip = -1;
+    if (cl > 1) cl_wait();
   }
   if (found && lane == 0) a.out_tokens[row] = token;
   if (rank == 0) {
@@ -385,6 +384,8 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
     }
   }
   __threadfence();   // no early trigger: the next step's calls read these lengths
+  __syncwarp();
+  if (cl > 1) cl_wait();
 }
 
 }  // namespace
