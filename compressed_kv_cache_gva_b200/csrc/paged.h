@@ -68,6 +68,7 @@ struct PagedArgs {
   void* out;
   float* lse;
   int out_bf16;
+  int wide;                               // out and the workspace are 32-byte aligned
   int* status;
   int flag_errors;                        // this kernel reports inconsistent sequences
   int beside;                             // runs beside the kernel before it (see pdl_enter)

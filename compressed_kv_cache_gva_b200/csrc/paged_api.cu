@@ -157,6 +157,7 @@ gva_status_t paged_attention(const gva_shape_t* shp, int page, const float* q_ab
   a.n_rows = n_rows; a.max_new = max_new;
   a.q_abs = q_abs; a.V = V; a.KR = KR; a.table = table; a.q_start = q_start; a.seq_len = seq_len;
   a.out = out; a.lse = lse; a.out_bf16 = sh.out_dtype == GVA_BF16;
+  a.wide = aligned(out, 32) && aligned(workspace, 32);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.status = reinterpret_cast<int*>(ws);
 

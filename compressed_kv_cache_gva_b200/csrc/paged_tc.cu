@@ -17,8 +17,8 @@
 //
 // Roles: warp 0 streams tiles with 2-D TMA loads, one box per page (or part of one),
 // its lanes holding the cache rows of the next 32 boxes; one thread of warp 1 issues
-// every MMA; warps 2 and 3 load the queries of the next piece; the warps from 4 on (one or
-// two per TMEM lane quarter) do the softmax, write P back to tensor memory (the A operand of the
+// every MMA; warps 2 and 3 (and the last four, where there are 16) load the queries of the
+// next piece; the warps from 4 on (one or two per TMEM lane quarter) do the softmax, write P back to tensor memory (the A operand of the
 // value product) and rescale O only when a row's maximum grew by more than 2^8.  While they exponentiate tile k, the MMA thread has
 // the scores of tile k + 1 computed.  All ring and buffer barriers count tiles over the
 // whole CTA, so they run on across pieces.
@@ -82,7 +82,11 @@ struct PtCfg {
   static constexpr uint32_t TMEM_COLS = 512 / PER_SM;
   static_assert(O_COL + D_H <= TMEM_COLS, "tensor memory");
   static constexpr uint32_t TX = VB + KRB;
-  static constexpr int THREADS = 128 + 128 * NH;
+  // Warps that load queries: 2 and 3, and four more where a CTA has the SM to itself and
+  // 128 registers a thread suffice.
+  static constexpr int LW = NH == 2 && PER_SM == 1 && !HILO ? 6 : 2;
+  static constexpr int QT = 32 * (LW + 4 * NH);             // with the softmax warps
+  static constexpr int THREADS = 64 + QT;
   static constexpr uint32_t SW_R = DRP == 32 ? tc::kSw64 : tc::kSw32;
   static constexpr uint32_t SBO_R = DRP * 2 * 8;
   // Two CTAs of 256 threads leave 128 registers a thread; a softmax warp holds 128 scores
@@ -222,6 +226,19 @@ __device__ __forceinline__ void prefetch_queries(const PagedArgs& a, const RowPi
   }
 }
 
+// 32 bytes of a row per lane, as one store where the buffers are 32-byte aligned: rows
+// lie apart, so each lane fills a whole sector instead of halves by two instructions.
+__device__ __forceinline__ void store_32b(void* dst, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // A softmax warp's place in the walk over the CTA's pieces.
 struct SoftmaxPiece {
   RowPiece p;
@@ -260,7 +277,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     }
     mbar_init(p_full, 4 * C::NH);
     mbar_init(pv_done, 1);
-    mbar_init(q_full, 2);
+    mbar_init(q_full, C::LW);
     mbar_init(q_free, 1);
     mbar_init(fin, 1);
     fence_barrier_init();
@@ -313,6 +330,23 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   // ok: false once a bounded wait gave up: skip work, keep the order.
   int kt = 0;
   bool ok = true;
+  // ------------------------------------------------------------ queries of the next piece
+  auto loader = [&]() {
+    const int tid = warp < 4 ? threadIdx.x - 64 : threadIdx.x - 64 - 128 * C::NH;
+    for (int i = 0; more; more = walk.next(), ++i) {
+      if (i > 0) {
+        prefetch_queries<C>(a, p, s, tid, 32 * C::LW);
+        ok = ok && mbar_wait(q_free, (i - 1) & 1, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        load_queries<C, 32 * C::LW>(a, p, s, sm, tid);
+      } else {   // the softmax warps have nothing else to do yet, and help
+        load_queries<C, C::QT>(a, p, s, sm, tid);
+        named_bar_sync(5, C::QT);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+  };
   if (warp < 4) {
     if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
@@ -419,23 +453,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       }
       __syncwarp();
     } else {
-      // ---------------------------------------------------------- queries of the next piece
-      for (int i = 0; more; more = walk.next(), ++i) {
-        if (i > 0) {
-          prefetch_queries<C>(a, p, s, threadIdx.x - 64, 64);
-          ok = ok && mbar_wait(q_free, (i - 1) & 1, a.status);
-          ok = __all_sync(0xffffffffu, ok);
-        }
-        // the softmax warps have nothing else to do before the first piece, and help
-        if (i > 0) load_queries<C, 64>(a, p, s, sm, threadIdx.x - 64);
-        else {
-          load_queries<C, C::THREADS - 64>(a, p, s, sm, threadIdx.x - 64);
-          named_bar_sync(5, C::THREADS - 64);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-      }
+      loader();
     }
+  } else if (warp >= 4 + 4 * C::NH) {
+    loader();
   } else {
     if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // One warp per lane quarter, or two that share its 32 rows, half of a tile's keys and
@@ -447,8 +468,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     __shared__ SoftmaxPiece pieces[4 * C::NH];
     SoftmaxPiece& sp = pieces[warp - 4];
     if (more) {
-      load_queries<C, C::THREADS - 64>(a, p, s, sm, threadIdx.x - 64);
-      named_bar_sync(5, C::THREADS - 64);
+      load_queries<C, C::QT>(a, p, s, sm, 32 * C::LW + threadIdx.x - 128);
+      named_bar_sync(5, C::QT);
       if (lane == 0) sp = SoftmaxPiece{walk.p, walk.s, walk.u, walk.end};
     }
     __syncwarp();
@@ -587,26 +608,26 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           tc::ld32(trow + C::O_COL + d0 + q * 32, o);
           tc::wait_ld();
           if (valid && ok) {
-            if (!whole) {
-              float4* dst = reinterpret_cast<float4*>(a.part_o + prt * C::D_H + d0 + q * 32);
+            if (!whole || !a.out_bf16) {
+              const float f = whole ? inv : 1.f;
+              float* dst = whole ? reinterpret_cast<float*>(a.out) + orow * C::D_H + d0 + q * 32
+                                 : a.part_o + prt * C::D_H + d0 + q * 32;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            } else if (a.out_bf16) {
-              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * C::D_H + d0 +
-                                                    q * 32);
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                    pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                    pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                    pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(o[i + j] * f);
+                store_32b(dst + i, w, a.wide);
+              }
             } else {
-              float4* dst =
-                  reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * C::D_H + d0 + q * 32);
+              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + orow * C::D_H + d0 + q * 32;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+              for (int i = 0; i < 32; i += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = pack_bf16(o[i + 2 * j] * inv, o[i + 2 * j + 1] * inv);
+                store_32b(dst + i, w, a.wide);
+              }
             }
           }
         }
