@@ -186,6 +186,11 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
           ok = false;
           break;
         }
+#ifdef GVA_TEST_WITHHOLD_TILE
+        // Failure-detection test builds only: this tile of every CTA is never requested
+        // (nothing is armed, no copy is in flight for it), so bounded waits run out.
+        if (k == GVA_TEST_WITHHOLD_TILE) continue;
+#endif
         const uint32_t fb = smem_u32(full + s), st = smem_u32(pipe + s * C::STAGE);
         if (lane == 0) mbar_arrive_expect_tx(fb, C::TX);
         __syncwarp();

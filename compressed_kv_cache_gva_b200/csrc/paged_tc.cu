@@ -154,7 +154,7 @@ struct QueryPart {
     const float* src = base + (R / (unsigned)hpr) * token + h * dq + c * 8;
     const int dh = STEP % hpr;   // the next row of this thread: STEP rows on
     const long long step = (STEP / hpr) * token + dh * dq, wrap = token - (long long)hpr * dq;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
       const int r = r0 + i * STEP;
       if (N * STEP == C::MS || r < C::MS) {
@@ -371,6 +371,11 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           if (kk >= C::STAGES) ok = mbar_wait(empty + 8 * sg, ((kk / C::STAGES) - 1) & 1, a.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+#ifdef GVA_TEST_WITHHOLD_TILE
+          // Failure-detection test builds only: this tile of every CTA is never requested
+          // (nothing is armed, no copy is in flight for it), so bounded waits run out.
+          if (kk == GVA_TEST_WITHHOLD_TILE) continue;
+#endif
           const uint32_t fb = full + 8 * sg, st = sb + C::OFF_RING + sg * C::STAGE;
           if (lane == 0) mbar_arrive_expect_tx(fb, C::TX);
           __syncwarp();
