@@ -79,9 +79,9 @@ struct PagedArgs {
 };
 
 bool paged_mma_supported(const gva_shape_t& sh, int page);
-int paged_mma_cols(const gva_shape_t& sh, int max_new);   // 4 or 8; 0: too many columns
+int paged_mma_cols(const gva_shape_t& sh, long long columns);   // 4, 8 or 16; 0: too many
 int paged_mma_tile(const gva_shape_t& sh);
-int paged_mma_grid(const gva_shape_t& sh, int max_new, int num_sms, long long max_total);
+int paged_mma_grid(const gva_shape_t& sh, int cols, int num_sms, long long max_total);
 cudaError_t launch_paged_mma(const gva_shape_t& sh, const PagedArgs& a, int cols,
                              const CUtensorMap& tv, const CUtensorMap& tk, cudaStream_t st);
 

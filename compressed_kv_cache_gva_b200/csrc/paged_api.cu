@@ -59,7 +59,7 @@ Share share(size_t at, size_t metas, size_t slots, size_t rows, size_t d_h) {
 }
 
 struct PagedPlan {
-  int cols;        // columns of the mma.sync kernel (4 or 8), 0: not launched
+  int cols;        // columns of the mma.sync kernel, 0: not launched
   int mma_new;     // most new tokens of a sequence it takes
   int mma_grid;
   enum { kNone, kTc, kSimt } rows;   // the row-block kernel
@@ -78,9 +78,15 @@ gva_status_t plan_paged(const gva_shape_t& sh, int page, int n_rows, int max_new
   const bool tc = !fma && gva::paged_tc_supported(sh, page);
   *p = PagedPlan{};
   p->rows = PagedPlan::kNone;
-  if (mma && (long long)max_new * hpr <= 8) {
-    p->cols = max_new * hpr <= 4 ? 4 : 8;
-  } else {
+  if (mma) p->cols = gva::paged_mma_cols(sh, (long long)max_new * hpr);
+  // Four groups of 16 columns take one CTA per SM.  A long batch of mostly single tokens
+  // streams faster through two, its few drafts beside it in row blocks: 64 x 1k-8k tokens
+  // with four new ones from every fourth request 65 us, 77 in one kernel; on 16 x 1k-8k
+  // 32 and 24 us, with 1 to 4 new tokens each on 64 x 1k-8k 90 and 78 us.
+  if (p->cols == 16 && sh.G == 4 && (long long)n_rows * hpr <= 8ll * sh.B &&
+      max_total * sh.G * sh.d_h * 2 >= (96ll << 20))
+    p->cols = 0;
+  if (!p->cols) {
     p->rows = tc ? PagedPlan::kTc : PagedPlan::kSimt;
     if (!tc && !gva::paged_simt_supported(sh))
       return refuse(GVA_ERR_UNSUPPORTED, "no paged attention kernel for H=%d G=%d d_h=%d d_r=%d", sh.H,

@@ -1,8 +1,8 @@
 // Paged split-KV attention of few query columns per value group (one new token per
 // request, or a few drafts), on mma.sync.
 //
-// A CTA is NG consumer warps (warp g: value group g and its query columns) and one
-// producer warp.  The batch's tiles of TT cached tokens are numbered in request order
+// A CTA is one consumer warp per value group and 8 of its query columns (two per group
+// for 9 to 16 columns) and one producer warp.  The batch's tiles of TT cached tokens are numbered in request order
 // and cut evenly over the CTAs; each tile is read once and serves every head.  The
 // producer resolves pages: its lanes hold the cache rows of the next 32 boxes (table
 // entries loaded one round ahead, so their latency hides behind the stream) and one
@@ -30,6 +30,9 @@ namespace {
 template <int D_H_, int NG_, int COLS_, int DRP_>
 struct PmCfg {
   static constexpr int D_H = D_H_, NG = NG_, COLS = COLS_, DRP = DRP_;
+  static constexpr int CPW = COLS < 8 ? COLS : 8;     // query columns of a warp
+  static constexpr int NJ = COLS / CPW;               // warps per group
+  static constexpr int NC = NG * NJ;                  // consumer warps
   static constexpr int ROW_BYTES = NG * D_H * 2;
   static constexpr int TT_RAW = 16384 / ROW_BYTES;
   static constexpr int TT = TT_RAW >= 64 ? 64 : (TT_RAW >= 32 ? 32 : 16);   // tokens per tile
@@ -41,34 +44,37 @@ struct PmCfg {
   static constexpr int XB = NG * CB * BOX;
   static constexpr int KRB = DRP * TT * 2;
   static constexpr int STAGE = XB + (KRB + 1023) / 1024 * 1024;
-  // 96 KB of ring for two CTAs per SM; the 33 KB tiles of eight 128-wide groups get a
-  // third stage (as in the unpaged kernel)
-  static constexpr int RING = (D_H == 128 && NG == 8) ? 108 * 1024 : 96 * 1024;
+  // 96 KB of ring for two CTAs per SM, 160 KB for one; the 33 KB tiles of eight 128-wide
+  // groups get a third stage (as in the unpaged kernel)
+  static constexpr bool ALONE = NJ > 1 && NG >= 4;
+  static constexpr int RING = ALONE ? 160 * 1024 : (D_H == 128 && NG == 8) ? 108 * 1024 : 96 * 1024;
   static constexpr int STAGES_RAW = RING / STAGE;
   static constexpr int STAGES = STAGES_RAW < 2 ? 2 : (STAGES_RAW > 12 ? 12 : STAGES_RAW);
   static constexpr int PIPE = STAGES * STAGE;
   static constexpr uint32_t TX = XB + KRB;
   static constexpr int MT = TT / 16;
-  static constexpr int THREADS = (NG + 1) * 32;
-  static constexpr int NT = COLS == 8 ? 2 : 1;
+  static constexpr int THREADS = (NC + 1) * 32;
+  static constexpr int NT = CPW == 8 ? 2 : 1;
   static constexpr int KS = D_H / 16, RS = DRP / 16;
   static constexpr int KR_SW = DRP * 2;
-  // 8 columns of d_h = 128 keep ~100 values live per consumer thread: one CTA per SM
-  static constexpr int MINB = (NG >= 8 && COLS == 8 && D_H == 128) ? 1 : 2;
+  // 8 columns of d_h = 128 keep ~100 values live per consumer thread: one CTA per SM,
+  // and so for two warps per group of four (26.8 against 29.9 us with two CTAs, which
+  // leave a thread 112 registers)
+  static constexpr int MINB = ALONE || (NG >= 8 && COLS == 8 && D_H == 128) ? 1 : 2;
   static size_t smem_bytes(int B) {
     return 1024 + PIPE + 16 * STAGES + sizeof(int) * (B + 1) + 16 + sizeof(long long) * 33;
   }
 };
 
 template <class C>
-__device__ __forceinline__ void load_query(const PagedArgs& a, const SeqRows& s, int g, int ncol, int gq,
+__device__ __forceinline__ void load_query(const PagedArgs& a, const SeqRows& s, int g, int c0, int ncol, int gq,
                                            int t, uint32_t (&qb)[C::NT][C::KS][2],
                                            uint32_t (&qr)[C::NT][C::RS > 0 ? C::RS : 1][2]) {
   const int dq = C::D_H + a.d_r;
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt) {
-    const int col = C::COLS == 8 ? gq : (gq & 3);
-    const bool lo = C::COLS == 8 ? nt == 1 : gq >= 4;
+    const int col = c0 + (C::CPW == 8 ? gq : (gq & 3));
+    const bool lo = C::CPW == 8 ? nt == 1 : gq >= 4;
     const bool on = col < ncol;   // padding columns carry a zero query
     const float* row =
         a.q_abs + ((long long)(s.r0 + (on ? col / a.hpr : 0)) * a.H + g * a.hpr + (on ? col % a.hpr : 0)) * dq;
@@ -115,11 +121,11 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(smem_u32(full + s), 1);
-      mbar_init(smem_u32(empty + s), C::NG);
+      mbar_init(smem_u32(empty + s), C::NC);
     }
     fence_barrier_init();
   }
-  if (warp == C::NG && lane == 0) {
+  if (warp == C::NC && lane == 0) {
     prefetch_tmap(&tm_v);
     if (C::DRP) prefetch_tmap(&tm_kr);
   }
@@ -160,7 +166,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   if (T1 <= T0) return;
   const int b_first = seq_at(tp, a.B, T0);
 
-  if (warp == C::NG) {
+  if (warp == C::NC) {
     // ---------------------------------------------------------------- producer
     const uint64_t pol = policy_evict_first();   // the cache is read once per call
     const int per_tile = C::TT >> a.box_log2;
@@ -214,11 +220,12 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   }
 
   // ------------------------------------------------------------------ consumers
-  const int g = warp, t = lane & 3, gq = lane >> 2, mi = lane >> 3, r8 = lane & 7;
+  const int g = warp % C::NG, c0 = warp / C::NG * C::CPW;   // this warp's group and first column
+  const int t = lane & 3, gq = lane >> 2, mi = lane >> 3, r8 = lane & 7;
   const int a_row = (mi & 1) * 8 + r8, a_kc = mi >> 1;   // scores A: rows = tokens
   const int v_tok = (mi >> 1) * 8 + r8, v_dc = mi & 1;   // P.V A (trans): rows = tokens
-  const bool lo_half = C::COLS == 4 && t >= 2;
-  const int hcol = (2 * t) & (C::COLS - 1);              // columns hcol, hcol + 1 after hi / lo merge
+  const bool lo_half = C::CPW == 4 && t >= 2;
+  const int hcol = c0 + ((2 * t) & (C::CPW - 1));        // columns hcol, hcol + 1 after hi / lo merge
   const int Hp = a.H * min(a.max_new, C::COLS / a.hpr);  // heads of a partial
   const int qi0 = hcol / a.hpr, qi1 = (hcol + 1) / a.hpr;
   const int head0 = g * a.hpr + hcol % a.hpr, head1 = g * a.hpr + (hcol + 1) % a.hpr;
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     const SeqRows sq = rows_of(b);
     const int ncol = sq.n * a.hpr;
     uint32_t qb[C::NT][C::KS][2], qr[C::NT][C::RS > 0 ? C::RS : 1][2];
-    load_query<C>(a, sq, g, ncol, gq, t, qb, qr);
+    load_query<C>(a, sq, g, c0, ncol, gq, t, qb, qr);
     const int lim0 = sq.L - sq.n + qi0, lim1 = sq.L - sq.n + qi1;   // last key of each column
     float o[C::KS][4];
 #pragma unroll
@@ -243,6 +250,11 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       const int s = k % C::STAGES, t0 = u * C::TT;
       if (ok) ok = mbar_wait(smem_u32(full + s), (k / C::STAGES) & 1, a.status);
       if (!ok) continue;
+      if (C::NJ > 1 && c0 >= ncol) {   // no query of this request is this warp's
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(empty + s));
+        continue;
+      }
       const int nvalid = min(C::TT, sq.L - t0);
       uint8_t* st = pipe + s * C::STAGE;
       uint8_t* xg = st + g * C::CB * C::BOX;
@@ -294,7 +306,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float x;
-          if constexpr (C::COLS == 8) x = (acc[0][0][e] + acc[1][0][e]) + (acc[0][1][e] + acc[1][1][e]);
+          if constexpr (C::CPW == 8) x = (acc[0][0][e] + acc[1][0][e]) + (acc[0][1][e] + acc[1][1][e]);
           else {
             x = acc[0][0][e] + acc[1][0][e];
             x += __shfl_xor_sync(0xffffffffu, x, 2);
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         rs0 += p0 + p2;
         rs1 += p1 + p3;
         const float h0 = bf16_round(p0), h1 = bf16_round(p1), h2 = bf16_round(p2), h3 = bf16_round(p3);
-        if constexpr (C::COLS == 8) {
+        if constexpr (C::CPW == 8) {
           bp[mm][0][0] = movm_t(pack_bf16(h0, h1));
           bp[mm][0][1] = movm_t(pack_bf16(h2, h3));
           bp[mm][1][0] = movm_t(pack_bf16(p0 - h0, p1 - h1));
@@ -377,7 +389,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       l0 += __shfl_xor_sync(0xffffffffu, l0, off);
       l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
-    if constexpr (C::COLS == 4) {
+    if constexpr (C::CPW == 4) {
 #pragma unroll
       for (int md = 0; md < C::KS; ++md)
 #pragma unroll
@@ -433,11 +445,16 @@ bool dispatch(const gva_shape_t& sh, int cols, F&& f) {
     return true;                                                                 \
   }
 #define GVA_PM_COLS(DH, NG, DRP) GVA_PM(DH, NG, 4, DRP) GVA_PM(DH, NG, 8, DRP)
-#define GVA_PM_NG(DH, DRP) GVA_PM_COLS(DH, 2, DRP) GVA_PM_COLS(DH, 4, DRP) GVA_PM_COLS(DH, 8, DRP)
+#define GVA_PM_NG(DH, DRP)                                                       \
+  GVA_PM_COLS(DH, 2, DRP) GVA_PM_COLS(DH, 4, DRP) GVA_PM_COLS(DH, 8, DRP) GVA_PM(DH, 2, 16, DRP)
 #define GVA_PM_DR(DH) GVA_PM_NG(DH, 0) GVA_PM_NG(DH, 16) GVA_PM_NG(DH, 32)
+#define GVA_PM_WIDE(DH) GVA_PM(DH, 4, 16, 0) GVA_PM(DH, 4, 16, 16) GVA_PM(DH, 4, 16, 32)
   GVA_PM_DR(32)
+  GVA_PM_WIDE(32)
   GVA_PM_DR(64)
+  GVA_PM_WIDE(64)
   GVA_PM_DR(128)
+#undef GVA_PM_WIDE
 #undef GVA_PM_DR
 #undef GVA_PM_NG
 #undef GVA_PM_COLS
@@ -450,6 +467,18 @@ bool dispatch(const gva_shape_t& sh, int cols, F&& f) {
 bool paged_mma_supported(const gva_shape_t& sh, int page) {
   if (sh.cache_dtype != GVA_BF16 || page % 8 || sh.H / sh.G > 8) return false;
   return dispatch(sh, 4, [](auto) {});
+}
+
+// Columns of the variant that takes `columns` per group (16: two warps per group, up to 4
+// groups and rows of 512 bytes), 0 if they are work for 128-row blocks.  Four new tokens of
+// four heads on 16 x 1k-8k and 4 x 512-2k tokens: d_h = 64, 4 groups 26.8 and 12.1 us (row
+// blocks 30.8 and 15.7), d_h = 128, 2 groups 25.6 and 12.9 us (32.9 and 16.5); 4 groups of
+// d_h = 128 42.4 and 18.0 us (46.3 and 17.0), on 64 x 1k-8k 140 (133).  With three warps per
+// group, five tokens took 32.6 us (31.9), on 64 x 1k-8k 100 (80): the split of the query
+// doubles products that mma.sync already bounds.
+int paged_mma_cols(const gva_shape_t& sh, long long columns) {
+  if (columns <= 8) return columns <= 4 ? 4 : 8;
+  return columns <= 16 && sh.G <= 4 && sh.G * sh.d_h <= 256 ? 16 : 0;
 }
 
 int paged_mma_tile(const gva_shape_t& sh) {

@@ -509,7 +509,8 @@ gva_status_t gva_plan_pages(int32_t B, int32_t page_size, int32_t num_pages, int
  * num_slots, is skipped and sets it too.
  *
  * Three kernels share the batch by new tokens per request:
- *  - up to 8 query columns (new tokens * H/G) per value group: split-KV over all SMs on
+ *  - up to 8 query columns (new tokens * H/G) per value group, up to 16 where
+ *    max_query_len allows no more, G <= 4 and G*d_h <= 256: split-KV over all SMs on
  *    mma.sync; bf16 cache, d_h in {32, 64, 128}, G in {2, 4, 8}, d_r <= 32;
  *  - more: row blocks of 128 query rows on tcgen05, split over the keys as well where
  *    there are few; bf16 cache, d_h in {64, 128}, d_r <= 32.  Probabilities are rounded
