@@ -2,13 +2,13 @@
 // request, or a few drafts), on mma.sync.
 //
 // A CTA is one consumer warp per value group and 8 of its query columns (two per group
-// for 9 to 16 columns) and one producer warp.  The batch's tiles of TT cached tokens are numbered in request order
-// and cut evenly over the CTAs; each tile is read once and serves every head.  The
-// producer resolves pages: its lanes hold the cache rows of the next 32 boxes (table
-// entries loaded one round ahead, so their latency hides behind the stream) and one
-// lane issues the 2-D TMA loads of a tile, TT / box boxes per 64 columns.  A box never
-// crosses a page, lands where the unpaged tile's rows would (8-row boxes keep the
-// 128-byte swizzle pattern), and reads zeros where there is no page.
+// for 9 to 16 columns) and one producer warp.  The batch's tiles of TT cached tokens are
+// numbered in request order and cut evenly over the CTAs; each tile is read once and
+// serves every head.  The producer resolves pages: its lanes hold the cache rows of the
+// next 32 boxes (table entries loaded one round ahead, so their latency hides behind the
+// stream) and one lane issues the 2-D TMA loads of a tile, TT / box boxes per 64
+// columns.  A box never crosses a page, lands where the unpaged tile's rows would (8-row
+// boxes keep the 128-byte swizzle pattern), and reads zeros where there is no page.
 //
 // Per tile and group, tokens on M and query columns on N (m16n8k16):
 //   S = V Qb (+ kr Qr),  online softmax in fp32 base 2,  O^T += V^T P.
