@@ -47,7 +47,7 @@ __device__ __forceinline__ void merge_seq(const PagedArgs& a, int b, int h, int 
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       if (c0 + u * npg >= n) break;
-      if (e[u].x == -INFINITY) continue;    // a piece past this query's last key
+      if (e[u].y == 0.f) continue;          // no key of the piece is this query's
       const float mn = fmaxf(m, e[u].x);
       const float f = ex2(m - mn), w = ex2(e[u].x - mn);
       l = l * f + w * e[u].y;
@@ -64,15 +64,14 @@ __device__ __forceinline__ void merge_seq(const PagedArgs& a, int b, int h, int 
   for (int u = 0; u < npg; ++u) M = fmaxf(M, sm_m[u][lane]);
   float L = 0.f, O = 0.f;
   for (int u = 0; u < npg; ++u) {
-    const float mu = sm_m[u][lane];
-    if (mu == -INFINITY) continue;
-    const float f = ex2(mu - M);
+    if (sm_l[u][lane] == 0.f) continue;
+    const float f = ex2(sm_m[u][lane] - M);
     L = fmaf(f, sm_l[u][lane], L);
     O = fmaf(f, sm_o[u][lane], O);
   }
   const long long orow = (long long)(r0 + qi) * a.H + h % a.H;
-  if (col) store_out(a, orow, d, L > 0.f ? O / L : 0.f);
-  if (lane == 0 && z == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  if (col) store_out(a, orow, d, L == 0.f ? 0.f : O / L);
+  if (lane == 0 && z == 0 && a.lse) a.lse[orow] = natural_lse(M, L);
 }
 
 // Row blocks cut between CTAs: the block that CTA i of the split started and did not end;
@@ -111,7 +110,7 @@ __device__ __forceinline__ void merge_rows(const PagedArgs& a, int i, int y, int
     }
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      if (ml[c].x == -INFINITY) continue;   // no piece, or one past this row's last key
+      if (ml[c].y == 0.f) continue;         // no piece, or none of its keys is this row's
       const float mn = fmaxf(m, ml[c].x);
       const float f = ex2(m - mn), w = ex2(ml[c].x - mn);
       l = l * f + w * ml[c].y;
@@ -122,7 +121,7 @@ __device__ __forceinline__ void merge_rows(const PagedArgs& a, int i, int y, int
   }
   const unsigned R = meta.w * M + r, qi = R / (unsigned)a.hpr;
   const long long orow = (long long)(where.x + (int)qi) * a.H + meta.z * a.hpr + (int)(R - qi * a.hpr);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = norm_of(l);
 #pragma unroll
   for (int u = 0; u < VEC; ++u) o[u] *= inv;
   if constexpr (VEC == 4) {
@@ -135,7 +134,7 @@ __device__ __forceinline__ void merge_rows(const PagedArgs& a, int i, int y, int
   } else {
     store_out(a, orow, d, o[0]);
   }
-  if (d == 0 && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (d == 0 && a.lse) a.lse[orow] = natural_lse(m, l);
 }
 
 // Both kinds in one launch: blocks [0, seq_blocks) take sequences, the rest row blocks.

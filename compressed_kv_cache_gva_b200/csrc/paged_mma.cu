@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       const float m = e ? m1 : m0, l = e ? l1 : l0;
       if (whole) {
         const long long orow = (long long)(sq.r0 + qi) * a.H + head;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = norm_of(l);
         if (a.out_bf16) {
           __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + orow * C::D_H + gq;
 #pragma unroll
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
             dst[md * 16 + 8] = o[md][e + 2] * inv;
           }
         }
-        if (gq == 0 && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (gq == 0 && a.lse) a.lse[orow] = natural_lse(m, l);
       } else {
         const long long ph = (long long)(blockIdx.x + b) * Hp + qi * a.H + head;
         float* dst = a.part_o + ph * C::D_H + gq;

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
     if (r < rows) {
       if (whole) {
         const long long orow = (long long)(s.r0 + qi) * a.H + head;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = norm_of(l);
 #pragma unroll
         for (int i = 0; i < COLS; ++i) {
           const int c = x + 16 * i;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedArgs a,
           if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[orow * d_h + c] = __float2bfloat16_rn(o[i] * inv);
           else reinterpret_cast<float*>(a.out)[orow * d_h + c] = o[i] * inv;
         }
-        if (x == 0 && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (x == 0 && a.lse) a.lse[orow] = natural_lse(m, l);
       } else {
         const long long slot = piece_slot(p, blockIdx.x);
         float* po = a.part_o + (slot * kM + r) * d_h;

@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         const int R = row0 + r, qi = R / hpr, head = sp.p.g * hpr + R % hpr;
         const long long orow = (long long)(sp.s.r0 + qi) * a.H + head;
         const long long prt = (long long)piece_slot(sp.p, blockIdx.x) * C::M + r;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = norm_of(l);
         const int d0 = half * C::HD;
 #pragma unroll
         for (int q = 0; q < C::HD / 32; ++q) {
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         }
         if (valid && ok && half == 0) {
           if (!whole) a.part_ml[prt] = make_float2(m, l);
-          else if (a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          else if (a.lse) a.lse[orow] = natural_lse(m, l);
         }
       }
       kt += nk;

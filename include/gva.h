@@ -503,6 +503,8 @@ gva_status_t gva_plan_pages(int32_t B, int32_t page_size, int32_t num_pages, int
  * Slots behind a request's end may hold anything, NaN included.  The request's own cached
  * tokens are finite: a NaN or infinity in one of them may reach every new token of the
  * request, those before it too (their probability of it is 0, and 0 x NaN is NaN).
+ * A query that holds a NaN makes its own row of out and lse NaN and no other (one that sees
+ * no key stays 0 and -inf); so does an infinity, unless all of the row's scores are -inf.
  * On the device: a page id outside the cache, or a request longer than its table row,
  * reads as 0 there and sets GVA_DEVERR_RANGE; a request whose row range is negative,
  * leaves [0, n_rows) or exceeds max_query_len, or whose length is negative or above
