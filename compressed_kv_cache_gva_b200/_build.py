@@ -40,8 +40,12 @@ def _deps():
 # Test-only variant for the failure-detection test: bounded pipeline waits give up
 # after 50 ms, and the split kernel's producer never requests the second tile of
 # each CTA, so a consumer wait runs out (no copy is ever in flight for that tile).
+# LANE_EXPIRY set in a paged call's status word makes waits run out in half of each
+# warp's lanes as well.
 WAIT_TEST_LIB = os.path.join(PKG, "libgva_waittest.so")
-WAIT_TEST_FLAGS = ("-DGVA_WAIT_NS=50000000ull", "-DGVA_TEST_WITHHOLD_TILE=1")
+LANE_EXPIRY = 1 << 30
+WAIT_TEST_FLAGS = ("-DGVA_WAIT_NS=50000000ull", "-DGVA_TEST_WITHHOLD_TILE=1",
+                   f"-DGVA_TEST_LANE_EXPIRY={LANE_EXPIRY}")
 
 
 def up_to_date(out: str = LIB) -> bool:

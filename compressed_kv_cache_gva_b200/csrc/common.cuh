@@ -479,6 +479,22 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* st
   return false;
 }
 
+// The same by a whole warp, with one answer for all lanes: a tile that lands just as the
+// limit runs out can be seen by some lanes and missed by others, and what follows a wait
+// (shuffles, matrix loads, tensor-memory accesses) needs the warp together.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
+  bool ok = mbar_wait(bar, parity, status);
+#ifdef GVA_TEST_LANE_EXPIRY
+  // Failure-detection test builds only: the host asks, by a bit of the status word, for waits
+  // that run out in half of the lanes.
+  if ((threadIdx.x & 1) && (*const_cast<volatile int*>(status) & GVA_TEST_LANE_EXPIRY)) {
+    atomicOr(status, GVA_DEVERR_WAIT);
+    ok = false;
+  }
+#endif
+  return __all_sync(0xffffffffu, ok);
+}
+
 // 2-D tiled TMA load global -> shared, completion counted on an mbarrier.
 // No multicast: every CTA fetches its own tiles.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,

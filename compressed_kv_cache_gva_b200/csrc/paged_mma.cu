@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
           y_next = look(base + 32 + lane);
         }
         const int s = k % C::STAGES;
-        if (k >= C::STAGES && !mbar_wait(smem_u32(empty + s), ((k / C::STAGES) - 1) & 1, a.status)) {
+        if (k >= C::STAGES && !mbar_wait_warp(smem_u32(empty + s), ((k / C::STAGES) - 1) & 1, a.status)) {
           ok = false;
           break;
         }
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 
     for (int u = u0; u < u1; ++u, ++k) {
       const int s = k % C::STAGES, t0 = u * C::TT;
-      if (ok) ok = mbar_wait(smem_u32(full + s), (k / C::STAGES) & 1, a.status);
+      if (ok) ok = mbar_wait_warp(smem_u32(full + s), (k / C::STAGES) & 1, a.status);
       if (!ok) continue;
       if (C::NJ > 1 && c0 >= ncol) {   // no query of this request is this warp's
         __syncwarp();

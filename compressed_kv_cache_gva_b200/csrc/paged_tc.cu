@@ -336,8 +336,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     for (int i = 0; more; more = walk.next(), ++i) {
       if (i > 0) {
         prefetch_queries<C>(a, p, s, tid, 32 * C::LW);
-        ok = ok && mbar_wait(q_free, (i - 1) & 1, a.status);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = ok && mbar_wait_warp(q_free, (i - 1) & 1, a.status);
         load_queries<C, 32 * C::LW>(a, p, s, sm, tid);
       } else {   // the softmax warps have nothing else to do yet, and help
         load_queries<C, C::QT>(a, p, s, sm, tid);
@@ -368,8 +367,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
             y_next = look(base + 32 + lane);
           }
           const int kk = kt + k, sg = kk % C::STAGES;
-          if (kk >= C::STAGES) ok = mbar_wait(empty + 8 * sg, ((kk / C::STAGES) - 1) & 1, a.status);
-          ok = __all_sync(0xffffffffu, ok);
+          if (kk >= C::STAGES) ok = mbar_wait_warp(empty + 8 * sg, ((kk / C::STAGES) - 1) & 1, a.status);
           if (!ok) break;
 #ifdef GVA_TEST_WITHHOLD_TILE
           // Failure-detection test builds only: this tile of every CTA is never requested
@@ -490,7 +488,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       float m = -INFINITY, l = 0.f;   // the row's reference; this half's sum
       for (int k = 0; k < nk; ++k) {
         const int kk = kt + k, sbuf = kk % C::NS, t0 = (k0 + k) * C::TK;
-        ok = ok && mbar_wait(s_full + 8 * sbuf, (kk / C::NS) & 1, a.status);
+        ok = ok && mbar_wait_warp(s_full + 8 * sbuf, (kk / C::NS) & 1, a.status);
         tc::fence_after();
         if (!idle) {
           float x[C::HK];
@@ -541,7 +539,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
                 lo[i] = pack_bf16(e.x - __uint_as_float(hi[i] << 16), e.y - __uint_as_float(hi[i] & 0xffff0000u));
             }
             if (q == 0 && kk >= 1) {   // P is free, and O still, once the P.V before has completed
-              ok = ok && mbar_wait(pv_done, (kk - 1) & 1, a.status);
+              ok = ok && mbar_wait_warp(pv_done, (kk - 1) & 1, a.status);
               tc::fence_after();
             }
             const uint32_t pc = trow + C::P_COL + half * (C::HK / 2) + q * 8;
@@ -569,7 +567,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           if (lane == 0) mbar_arrive(s_free + 8 * sbuf);
           // keep step with the warps that write P: an arrival for this tile must not
           // count for the one before
-          if (kk >= 1) ok = ok && mbar_wait(pv_done, (kk - 1) & 1, a.status);
+          if (kk >= 1) ok = ok && mbar_wait_warp(pv_done, (kk - 1) & 1, a.status);
         }
         // value rows behind the sequence meet P = 0 but may hold anything (NaN): zero
         // them before the P.V product reads them
@@ -589,10 +587,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       }
       {   // the last P.V of the piece (and with it every MMA before) has completed
         const int kl = kt + nk - 1;
-        ok = ok && mbar_wait(pv_done, kl & 1, a.status);
+        ok = ok && mbar_wait_warp(pv_done, kl & 1, a.status);
         tc::fence_after();
       }
-      ok = __all_sync(0xffffffffu, ok);
       if (!idle) {
         if constexpr (C::NH == 2) {   // the halves' sums, through the buffer of the next tile
           const int xb = (kt + nk) & 1;
