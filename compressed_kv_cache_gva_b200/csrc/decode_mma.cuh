@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     for (int t0 = j0; t0 < j1; t0 += C::TT, ++k) {
       if (k % C::W != w) continue;                 // another warp of the group takes it
       const int s = k % C::STAGES;
-      if (ok) ok = mbar_wait(smem_u32(full + s), (k / C::STAGES) & 1, a.status);
+      if (ok) ok = mbar_wait_warp(smem_u32(full + s), (k / C::STAGES) & 1, a.status);
       if (!ok) continue;
       if (warp == 0 && lane == 0 && k == 0) trace_mark(a, 3);
       if (warp == 0 && lane == 0) trace_tile(a, k, 1);
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   // own slot, until the empty-pool mark
   while (n_pool > 0 && ok) {
     const int s = k % C::STAGES;
-    ok = mbar_wait(smem_u32(full + s), (k / C::STAGES) & 1, a.status);
+    ok = mbar_wait_warp(smem_u32(full + s), (k / C::STAGES) & 1, a.status);
     if (!ok) break;
     const int v = *static_cast<volatile int*>(pool_tile + s);
     if (v < 0) break;

@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     for (int b = b_first; rng.reaches(b); ++b) {
       int j0, j1;
       if (!rng.piece(b, j0, j1)) continue;
-      if (n >= 2 && !mbar_wait(q_free + 8 * (n & 1), ((n - 2) >> 1) & 1, a.status)) break;
+      if (n >= 2 && !mbar_wait_warp(q_free + 8 * (n & 1), ((n - 2) >> 1) & 1, a.status)) break;
       uint8_t* qt = sm + C::OFF_Q + (n & 1) * C::QBUF;
       for (int e = tid; e < C::NS * (C::D_H / 8); e += 64) {
         const int r = e / (C::D_H / 8), ch = e % (C::D_H / 8);
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       const int nvalid = min(C::TT, j1 - t.t0);
       const bool valid = tok < nvalid;
       const int sbuf = k % C::NSB, pb = k % C::NPB;
-      ok = ok && mbar_wait(s_full + 8 * sbuf, (k / C::NSB) & 1, a.status);
+      ok = ok && mbar_wait_warp(s_full + 8 * sbuf, (k / C::NSB) & 1, a.status);
       tc::fence_after();
       if (threadIdx.x == 128) tc_trace(a, k, 2);
       float sv[8];
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       }
       // P buffer k % NPB is free once the P.V of tile k - NPB has completed
       if (k >= C::NPB) {
-        ok = ok && mbar_wait(pv_done + 8 * pb, ((k / C::NPB) - 1) & 1, a.status);
+        ok = ok && mbar_wait_warp(pv_done + 8 * pb, ((k / C::NPB) - 1) & 1, a.status);
         tc::fence_after();
       }
       if (threadIdx.x == 128) tc_trace(a, k, 3);
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
           if (resc_tag[(k & 1) * C::G + gg] != k + 1) continue;
           if (!waited) {
             // O holds every P.V up to tile k - 1
-            ok = ok && mbar_wait(pv_done + 8 * ((k - 1) % C::NPB), ((k - 1) / C::NPB) & 1, a.status);
+            ok = ok && mbar_wait_warp(pv_done + 8 * ((k - 1) % C::NPB), ((k - 1) / C::NPB) & 1, a.status);
             tc::fence_after();
             waited = true;
           }
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 
       if (last) {
         // ---- piece epilogue: (m, l) per head, and O once its last P.V completed
-        ok = ok && mbar_wait(pv_done + 8 * pb, (k / C::NPB) & 1, a.status);
+        ok = ok && mbar_wait_warp(pv_done + 8 * pb, (k / C::NPB) & 1, a.status);
         tc::fence_after();
 #pragma unroll
         for (int o = 1; o < gw; o <<= 1)

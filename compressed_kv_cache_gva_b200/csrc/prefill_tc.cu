@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int k = 0; k < ntiles; ++k) {
-      ok = ok && mbar_wait(s_full + 8 * (k & 1), (k >> 1) & 1, a.status);
+      ok = ok && mbar_wait_warp(s_full + 8 * (k & 1), (k >> 1) & 1, a.status);
       tc::fence_after();
       float s[C::TK];
 #pragma unroll
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // P buffer k % 2 is free once the P.V of tile k - 2 has completed
       const int pb = k & 1;
       if (k >= 2) {
-        ok = ok && mbar_wait(pv_done + 8 * pb, ((k - 2) >> 1) & 1, a.status);
+        ok = ok && mbar_wait_warp(pv_done + 8 * pb, ((k - 2) >> 1) & 1, a.status);
         tc::fence_after();
       }
       // P in bf16, one swizzled 16-byte chunk (8 keys) at a time
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // O *= alpha before this tile's P.V accumulates onto it, once the previous
       // P.V has completed (only when some row of the warp raised its max)
       if (k >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        ok = ok && mbar_wait(pv_done + 8 * ((k - 1) & 1), ((k - 1) >> 1) & 1, a.status);
+        ok = ok && mbar_wait_warp(pv_done + 8 * ((k - 1) & 1), ((k - 1) >> 1) & 1, a.status);
         tc::fence_after();
 #pragma unroll
         for (int q4 = 0; q4 < C::D_H / 16; ++q4) {
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (lane == 0) mbar_arrive(p_full + 8 * pb);
     }
     if (ntiles > 0) {   // the last P.V (and with it every earlier one) has completed
-      ok = ok && mbar_wait(pv_done + 8 * ((ntiles - 1) & 1), ((ntiles - 1) >> 1) & 1, a.status);
+      ok = ok && mbar_wait_warp(pv_done + 8 * ((ntiles - 1) & 1), ((ntiles - 1) >> 1) & 1, a.status);
       tc::fence_after();
     }
     // ---- output: O / l (zero and lse = -inf for a query that sees no cache row)
