@@ -218,16 +218,18 @@ __global__ void __launch_bounds__(kPlanMaxThreads) plan_pages_kernel(const PlanA
     return idx < count ? a.free_pages[idx] : returned(idx - count);
   };
   // Tokens, kTok per thread at a time: their searches and table reads are independent
-  // chains that overlap.
-  for (int i0 = gid; i0 < a.max_new; i0 += kTok * gt) {
+  // chains that overlap.  (These loops step past their ends, so their counters are
+  // unsigned: tokens and pages may number 2^31 - 1.)
+  const unsigned step = (unsigned)gt, room = (unsigned)a.max_new;
+  for (unsigned i0 = gid; i0 < room; i0 += kTok * step) {
     int p[kTok], pg[kTok];
 #pragma unroll
     for (int u = 0; u < kTok; ++u) {
-      const int i = i0 + u * gt;
+      const unsigned i = i0 + u * step;
       p[u] = pg[u] = -1;
-      if (i < n_tokens) {
-        const int b = owner_of(qs, B, i);
-        p[u] = kept[b] + (i - qs[b]);
+      if (i < (unsigned)n_tokens) {
+        const int b = owner_of(qs, B, (int)i);
+        p[u] = kept[b] + ((int)i - qs[b]);
         const int col = p[u] / a.page;
         pg[u] = col < held[b] ? a.table[(long long)b * a.table_stride + col]
                               : page_of_rank(np[b] + col - held[b]);
@@ -235,17 +237,17 @@ __global__ void __launch_bounds__(kPlanMaxThreads) plan_pages_kernel(const PlanA
     }
 #pragma unroll
     for (int u = 0; u < kTok; ++u) {
-      const int i = i0 + u * gt;
-      if (i >= a.max_new) break;
+      const unsigned i = i0 + u * step;
+      if (i >= room) break;
       const bool ok = pg[u] >= 0 && pg[u] < a.num_pages;
-      if (!ok && i < n_tokens && a.err_flag) atomicOr(a.err_flag, GVA_DEVERR_RANGE);
+      if (!ok && i < (unsigned)n_tokens && a.err_flag) atomicOr(a.err_flag, GVA_DEVERR_RANGE);
       a.slot[i] = ok ? pg[u] * a.page + p[u] % a.page : -1;
       a.pos[i] = p[u];
     }
   }
-  for (int k = gid; k < n_back; k += gt) a.free_pages[count + k] = returned(k);
-  for (int r = gid; r < n_pages; r += gt) {
-    const int b = owner_of(np, B, r);
+  for (unsigned k = gid; k < (unsigned)n_back; k += step) a.free_pages[count + k] = returned((int)k);
+  for (unsigned q = gid; q < (unsigned)n_pages; q += step) {
+    const int r = (int)q, b = owner_of(np, B, r);
     a.table[(long long)b * a.table_stride + held[b] + (r - np[b])] = page_of_rank(r);
   }
   // No early trigger: slots, positions and lengths are inputs that the next call's
