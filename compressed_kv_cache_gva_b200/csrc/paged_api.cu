@@ -290,7 +290,9 @@ gva_status_t gva_verify_draft(int32_t B, int32_t vocab, int32_t n_rows, const in
                               int32_t* err_flag, void* stream) {
   if (B < 0 || B > 65535) return refuse(GVA_ERR_INVALID_ARG, "B=%d outside [0, 65535]", B);
   if (vocab < 1 || vocab > (1 << 30)) return refuse(GVA_ERR_INVALID_ARG, "vocab=%d outside [1, 2^30]", vocab);
-  if (n_rows < 0) return refuse(GVA_ERR_INVALID_ARG, "n_rows=%d < 0", n_rows);
+  // (a block's loop over a request's rows counts up to its width past the last)
+  if (n_rows < 0 || n_rows > INT32_MAX - 1024)
+    return refuse(GVA_ERR_INVALID_ARG, "n_rows=%d outside [0, 2^31 - 1025]", n_rows);
   if (probs_dtype != GVA_F32 && probs_dtype != GVA_BF16)
     return refuse(GVA_ERR_INVALID_ARG, "probs_dtype must be GVA_F32 or GVA_BF16");
   if (target_stride < vocab || (draft_probs && draft_stride < vocab))

@@ -555,7 +555,7 @@ gva_status_t gva_paged_attention(const gva_shape_t* shape, int32_t page_size, co
  * sums in 64 bits.  Weights that are not > 0, NaN included, count as 0; weights are
  * otherwise finite.
  *
- *   vocab      > 0;  n_rows: rows of the buffers;  B in [0, 65535]
+ *   vocab      in [1, 2^30];  n_rows: rows of the buffers, at most 2^31 - 1025;  B in [0, 65535]
  *   tokens     device [n_rows] int32: the fed tokens
  *   q_start    device [B + 1] int32, as gva_paged_attention; a request may have no rows
  *   target_probs, draft_probs   device [n_rows, vocab] probs_dtype, rows target_stride /
