@@ -141,6 +141,19 @@ __device__ __forceinline__ void fetch(const T* row, int v, int n, bool vec, uint
   else
     *reinterpret_cast<uint4*>(at) = load_vec(row, v, n, false);
 }
+// The lane's part of a chunk, every weight in 64 bits: where pairs exceed the largest float
+// (weights need not be normalised).
+template <typename T>
+__device__ __noinline__ double lane_sum_wide(const Weights<T> W, int v0, int v1, int lane) {
+  constexpr int N = RowVec<T>::N, SEG = 32 * N;
+  double sum = 0.0;
+  for (int v = v0 + lane * N; v - lane * N < v1; v += SEG) {
+    double w[N];
+    W.get(v, W.load_p(v), W.load_q(v), w);
+    for (int j = 0; j < N; ++j) sum += w[j];
+  }
+  return sum;
+}
 template <typename T, bool Q>
 __device__ __forceinline__ double chunk_sum_of(const Weights<T>& W, int v0, int v1, uint8_t* ring, int lane) {
   constexpr int N = RowVec<T>::N, SEG = 32 * N, S = Q ? kVfUnits / 2 : kVfUnits;
@@ -181,7 +194,9 @@ __device__ __forceinline__ double chunk_sum_of(const Weights<T>& W, int v0, int 
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");   // the ring is free again
-  return warp_sum(acc + (double)rest);
+  double sum = acc + (double)rest;
+  if (!isfinite(sum)) sum = lane_sum_wide(W, v0, v1, lane);
+  return warp_sum(sum);
 }
 template <typename T>
 __device__ __forceinline__ double chunk_sum(const Weights<T>& W, int v0, int v1, uint8_t* ring, int lane) {
