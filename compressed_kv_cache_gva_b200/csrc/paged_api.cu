@@ -309,6 +309,10 @@ gva_status_t gva_verify_draft(int32_t B, int32_t vocab, int32_t n_rows, const in
   const int e = probs_dtype == GVA_F32 ? 4 : 2;
   if (!aligned(target_probs, e) || !aligned(draft_probs, e))
     return refuse(GVA_ERR_INVALID_ARG, "probabilities must be aligned to their type");
+  // the CTAs of a request read its tokens at their own pace while the first writes the result
+  const uintptr_t t0 = reinterpret_cast<uintptr_t>(tokens), o0 = reinterpret_cast<uintptr_t>(out_tokens);
+  if (n_rows > 0 && t0 < o0 + 4ull * n_rows && o0 < t0 + 4ull * n_rows)
+    return refuse(GVA_ERR_INVALID_ARG, "out_tokens must not overlap tokens");
   const int sms = gva::device_sms();
   if (sms <= 0) return refuse(GVA_ERR_CUDA, "no CUDA device");
   gva::VerifyArgs a{};

@@ -562,7 +562,8 @@ gva_status_t gva_paged_attention(const gva_shape_t* shape, int32_t page_size, co
  *              draft_stride (>= vocab) elements apart, no alignment beyond the element's
  *   u_accept   device [n_rows] float32 in [0, 1);  u_sample device [B] float32 in [0, 1)
  *   out_tokens device [n_rows] int32: the accepted drafts, then the new token, then -1,
- *              from q_start[b]; rows of no request are left as they were
+ *              from q_start[b]; rows of no request are left as they were; must not overlap
+ *              tokens
  *   n_accepted device [B] int32: a (0 for a request without rows)
  *   seq_len, kept_len   device [B] int32, both or neither: kept_len = seq_len - (k - a),
  *              the cached tokens that stay (may be the same buffer)
