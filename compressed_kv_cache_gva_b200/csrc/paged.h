@@ -81,7 +81,8 @@ struct PagedArgs {
 bool paged_mma_supported(const gva_shape_t& sh, int page);
 int paged_mma_cols(const gva_shape_t& sh, long long columns);   // 4, 8 or 16; 0: too many
 int paged_mma_tile(const gva_shape_t& sh);
-int paged_mma_grid(const gva_shape_t& sh, int cols, int num_sms, long long max_total);
+// (cap_B: the batch whose prefix array decides how many CTAs fit an SM)
+int paged_mma_grid(const gva_shape_t& sh, int cols, int num_sms, long long max_total, int cap_B);
 cudaError_t launch_paged_mma(const gva_shape_t& sh, const PagedArgs& a, int cols,
                              const CUtensorMap& tv, const CUtensorMap& tk, cudaStream_t st);
 
@@ -92,7 +93,7 @@ cudaError_t launch_paged_tc(const gva_shape_t& sh, const PagedArgs& a, const CUt
                             const CUtensorMap& tk, cudaStream_t st);
 
 bool paged_simt_supported(const gva_shape_t& sh);
-int paged_simt_grid(const gva_shape_t& sh, int n_rows, int num_sms, long long max_total);
+int paged_simt_grid(const gva_shape_t& sh, int n_rows, int num_sms, long long max_total, int cap_B);
 cudaError_t launch_paged_simt(const gva_shape_t& sh, const PagedArgs& a, cudaStream_t st);
 
 constexpr int kPagedTcRows = 128;         // query rows (token x head) of a tcgen05 block

@@ -47,11 +47,12 @@ bool aligned(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n
 // One kernel's share of the workspace: piece records, (max, sum) and outputs.
 struct Share {
   size_t meta, ml, o, end;
+  Share after(size_t at) const { return Share{at + meta, at + ml, at + o, at + end}; }   // (at: a multiple of 256)
 };
 
-Share share(size_t at, size_t metas, size_t slots, size_t rows, size_t d_h) {
+Share share(size_t metas, size_t slots, size_t rows, size_t d_h) {
   Share s;
-  s.meta = gva::align_up(at, 256);
+  s.meta = 0;
   s.ml = gva::align_up(s.meta + sizeof(int4) * metas, 256);
   s.o = gva::align_up(s.ml + sizeof(float2) * slots * rows, 256);
   s.end = gva::align_up(s.o + sizeof(float) * slots * rows * d_h, 256);
@@ -68,24 +69,70 @@ struct PagedPlan {
   size_t total;
 };
 
+bool uses_mma(const gva_shape_t& sh, int page) {
+  return !(sh.flags & GVA_FLAG_FMA_PATH) && gva::paged_mma_supported(sh, page);
+}
+bool uses_tc(const gva_shape_t& sh, int page) {
+  return !(sh.flags & GVA_FLAG_FMA_PATH) && gva::paged_tc_supported(sh, page);
+}
+
+// Four groups of 16 columns take one CTA per SM.  A long batch of mostly single tokens
+// streams faster through two, its few drafts beside it in row blocks: 64 x 1k-8k tokens
+// with four new ones from every fourth request 65 us, 77 in one kernel; on 16 x 1k-8k
+// 32 and 24 us, with 1 to 4 new tokens each on 64 x 1k-8k 90 and 78 us.
+bool long_batch(const gva_shape_t& sh, long long max_total) {
+  return sh.G == 4 && max_total * sh.G * sh.d_h * 2 >= (96ll << 20);
+}
+
+// The shares of the kernels, from 0 on.  cap_B: see the grids.
+Share mma_share(const gva_shape_t& sh, int cols, int max_new, int sms, long long max_total, int cap_B,
+                PagedPlan* p) {
+  const int hpr = sh.H / sh.G;
+  p->mma_new = cols / hpr < max_new ? cols / hpr : max_new;
+  p->mma_grid = gva::paged_mma_grid(sh, cols, sms, max_total, cap_B);
+  return share(sh.B, (size_t)p->mma_grid + sh.B, (size_t)sh.H * p->mma_new, sh.d_h);
+}
+Share rows_share(const gva_shape_t& sh, bool tc, int n_rows, int max_new, int sms, long long max_total,
+                 int cap_B, PagedPlan* p) {
+  p->rows_grid = tc ? gva::paged_tc_grid(sh, n_rows, max_new, sms, max_total)
+                    : gva::paged_simt_grid(sh, n_rows, sms, max_total, cap_B);
+  const size_t g = 2 * (size_t)p->rows_grid;
+  return share(g, g, tc ? gva::kPagedTcRows : gva::kPagedSimtRows, sh.d_h);
+}
+constexpr size_t kPagedHead = 256;   // the status word
+
+// Bytes that serve every call of these heads and types whose B, n_rows, max_new and
+// max_total are no larger.  A single plan's bytes do not: fewer new tokens may take the
+// split-KV kernel, with a state per CTA and head, where more take row blocks.
+size_t most_paged(const gva_shape_t& sh, int page, int n_rows, int max_new, int sms, long long max_total) {
+  const int hpr = sh.H / sh.G;
+  PagedPlan p{};
+  size_t split = 0;
+  bool rows = true;
+  if (uses_mma(sh, page)) {
+    rows = gva::paged_mma_cols(sh, (long long)max_new * hpr) == 0;
+    for (int cols = 4; cols <= 16; cols *= 2) {
+      if (cols < hpr || (cols == 16 && gva::paged_mma_cols(sh, 16) != 16)) continue;
+      const size_t end = mma_share(sh, cols, max_new, sms, max_total, 1, &p).end;
+      split = end > split ? end : split;
+    }
+    const int first16 = 8 / hpr + 1;   // the fewest new tokens that take 16 columns, if any do
+    if (first16 <= max_new && gva::paged_mma_cols(sh, (long long)first16 * hpr) == 16 && long_batch(sh, max_total))
+      rows = true;
+  }
+  return kPagedHead + split + (rows ? rows_share(sh, uses_tc(sh, page), n_rows, max_new, sms, max_total, 1, &p).end : 0);
+}
+
 gva_status_t plan_paged(const gva_shape_t& sh, int page, int n_rows, int max_new, long long max_total,
                         PagedPlan* p) {
   const int sms = gva::device_sms();
   if (sms <= 0) return refuse(GVA_ERR_CUDA, "no CUDA device");
   const int hpr = sh.H / sh.G;
-  const bool fma = sh.flags & GVA_FLAG_FMA_PATH;
-  const bool mma = !fma && gva::paged_mma_supported(sh, page);
-  const bool tc = !fma && gva::paged_tc_supported(sh, page);
+  const bool mma = uses_mma(sh, page), tc = uses_tc(sh, page);
   *p = PagedPlan{};
   p->rows = PagedPlan::kNone;
   if (mma) p->cols = gva::paged_mma_cols(sh, (long long)max_new * hpr);
-  // Four groups of 16 columns take one CTA per SM.  A long batch of mostly single tokens
-  // streams faster through two, its few drafts beside it in row blocks: 64 x 1k-8k tokens
-  // with four new ones from every fourth request 65 us, 77 in one kernel; on 16 x 1k-8k
-  // 32 and 24 us, with 1 to 4 new tokens each on 64 x 1k-8k 90 and 78 us.
-  if (p->cols == 16 && sh.G == 4 && (long long)n_rows * hpr <= 8ll * sh.B &&
-      max_total * sh.G * sh.d_h * 2 >= (96ll << 20))
-    p->cols = 0;
+  if (p->cols == 16 && (long long)n_rows * hpr <= 8ll * sh.B && long_batch(sh, max_total)) p->cols = 0;
   if (!p->cols) {
     p->rows = tc ? PagedPlan::kTc : PagedPlan::kSimt;
     if (!tc && !gva::paged_simt_supported(sh))
@@ -95,21 +142,15 @@ gva_status_t plan_paged(const gva_shape_t& sh, int page, int n_rows, int max_new
     // them brings max_new (the rows then fill all of n_rows).
     if (mma && (long long)sh.B * max_new > n_rows) p->cols = hpr <= 4 ? 4 : 8;
   }
-  size_t at = 256;
+  p->total = kPagedHead;
   if (p->cols) {
-    p->mma_new = p->cols / hpr < max_new ? p->cols / hpr : max_new;
-    p->mma_grid = gva::paged_mma_grid(sh, p->cols, sms, max_total);
-    p->mma = share(at, sh.B, (size_t)p->mma_grid + sh.B, (size_t)sh.H * p->mma_new, sh.d_h);
-    at = p->mma.end;
+    p->mma = mma_share(sh, p->cols, max_new, sms, max_total, sh.B, p).after(p->total);
+    p->total = p->mma.end;
   }
   if (p->rows != PagedPlan::kNone) {
-    const int M = p->rows == PagedPlan::kTc ? gva::kPagedTcRows : gva::kPagedSimtRows;
-    p->rows_grid = p->rows == PagedPlan::kTc ? gva::paged_tc_grid(sh, n_rows, max_new, sms, max_total)
-                                             : gva::paged_simt_grid(sh, n_rows, sms, max_total);
-    p->blk = share(at, 2 * (size_t)p->rows_grid, 2 * (size_t)p->rows_grid, M, sh.d_h);
-    at = p->blk.end;
+    p->blk = rows_share(sh, tc, n_rows, max_new, sms, max_total, sh.B, p).after(p->total);
+    p->total = p->blk.end;
   }
-  p->total = at;
   return GVA_OK;
 }
 
@@ -264,7 +305,8 @@ size_t gva_paged_workspace_size(const gva_shape_t* shape, int32_t page_size, int
   if (shape->B == 0 || n_rows == 0) return 256;
   PagedPlan p;
   const int most = max_query_len < n_rows ? max_query_len : n_rows;
-  return plan_paged(*shape, page_size, n_rows, most, max_total_tokens, &p) == GVA_OK ? p.total : 0;
+  if (plan_paged(*shape, page_size, n_rows, most, max_total_tokens, &p) != GVA_OK) return 0;
+  return most_paged(*shape, page_size, n_rows, most, gva::device_sms(), max_total_tokens);
 }
 
 gva_status_t gva_paged_attention(const gva_shape_t* shape, int32_t page_size, const float* q_abs,

@@ -487,13 +487,13 @@ int paged_mma_tile(const gva_shape_t& sh) {
   return tt;
 }
 
-int paged_mma_grid(const gva_shape_t& sh, int cols, int num_sms, long long max_total) {
+int paged_mma_grid(const gva_shape_t& sh, int cols, int num_sms, long long max_total, int cap_B) {
   int tt = 16, minb = 2;
   size_t smem = 0;
   dispatch(sh, cols, [&](auto c) {
     tt = decltype(c)::TT;
     minb = decltype(c)::MINB;
-    smem = decltype(c)::smem_bytes(sh.B);
+    smem = decltype(c)::smem_bytes(cap_B);
   });
   int per_sm = (int)((227 * 1024) / (smem + 1024));
   per_sm = per_sm < 1 ? 1 : (per_sm > minb ? minb : per_sm);

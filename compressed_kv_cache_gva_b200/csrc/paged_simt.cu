@@ -195,8 +195,8 @@ bool paged_simt_supported(const gva_shape_t& sh) {
   return sh.d_h <= kMaxD && simt_smem(sh.B, sh.d_h, sh.d_r).total <= 200 * 1024;
 }
 
-int paged_simt_grid(const gva_shape_t& sh, int n_rows, int num_sms, long long max_total) {
-  const size_t smem = simt_smem(sh.B, sh.d_h, sh.d_r).total;
+int paged_simt_grid(const gva_shape_t& sh, int n_rows, int num_sms, long long max_total, int cap_B) {
+  const size_t smem = simt_smem(cap_B, sh.d_h, sh.d_r).total;
   int per_sm = (int)((220 * 1024) / (smem + 1024));
   per_sm = per_sm < 1 ? 1 : (per_sm > 3 ? 3 : per_sm);
   if (sh.ctas_per_sm > 0) per_sm = sh.ctas_per_sm;

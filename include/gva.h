@@ -497,7 +497,9 @@ gva_status_t gva_plan_pages(int32_t B, int32_t page_size, int32_t num_pages, int
  *   out, lse   device [n_rows, H, d_h] out_dtype and [n_rows, H] float32 or NULL, as
  *              gva_decode_attention; rows of no request (from q_start[B] on) are left
  *              as they were
- *   workspace  zeroed once; gva_paged_workspace_size bytes; its first word is the
+ *   workspace  zeroed once; gva_paged_workspace_size bytes, which serve every call with the
+ *              same heads, types, flags and page_size whose B, n_rows, max_query_len and
+ *              max_total_tokens are no larger; its first word is the
  *              status word (GVA_DEVERR_*), as for gva_decode_attention.  Calls that may
  *              overlap on the GPU (streams, or graphs) must use different workspaces.
  * Slots behind a request's end may hold anything, NaN included.  The request's own cached
