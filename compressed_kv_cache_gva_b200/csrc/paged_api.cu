@@ -79,9 +79,11 @@ bool uses_tc(const gva_shape_t& sh, int page) {
 // Four groups of 16 columns take one CTA per SM.  A long batch of mostly single tokens
 // streams faster through two, its few drafts beside it in row blocks: 64 x 1k-8k tokens
 // with four new ones from every fourth request 65 us, 77 in one kernel; on 16 x 1k-8k
-// 32 and 24 us, with 1 to 4 new tokens each on 64 x 1k-8k 90 and 78 us.
-bool long_batch(const gva_shape_t& sh, long long max_total) {
-  return sh.G == 4 && max_total * sh.G * sh.d_h * 2 >= (96ll << 20);
+// 32 and 24 us, with 1 to 4 new tokens each on 64 x 1k-8k 90 and 78 us.  Only where row
+// blocks run on tcgen05: with d_h = 32 they would take the CUDA cores, 322 us instead of 82
+// for 64 x 6k-8k tokens with four new ones from every fourth request.
+bool long_batch(const gva_shape_t& sh, int page, long long max_total) {
+  return sh.G == 4 && uses_tc(sh, page) && max_total * sh.G * sh.d_h * 2 >= (96ll << 20);
 }
 
 // The shares of the kernels, from 0 on.  cap_B: see the grids.
@@ -117,7 +119,8 @@ size_t most_paged(const gva_shape_t& sh, int page, int n_rows, int max_new, int 
       split = end > split ? end : split;
     }
     const int first16 = 8 / hpr + 1;   // the fewest new tokens that take 16 columns, if any do
-    if (first16 <= max_new && gva::paged_mma_cols(sh, (long long)first16 * hpr) == 16 && long_batch(sh, max_total))
+    if (first16 <= max_new && gva::paged_mma_cols(sh, (long long)first16 * hpr) == 16 &&
+        long_batch(sh, page, max_total))
       rows = true;
   }
   return kPagedHead + split + (rows ? rows_share(sh, uses_tc(sh, page), n_rows, max_new, sms, max_total, 1, &p).end : 0);
@@ -132,7 +135,7 @@ gva_status_t plan_paged(const gva_shape_t& sh, int page, int n_rows, int max_new
   *p = PagedPlan{};
   p->rows = PagedPlan::kNone;
   if (mma) p->cols = gva::paged_mma_cols(sh, (long long)max_new * hpr);
-  if (p->cols == 16 && (long long)n_rows * hpr <= 8ll * sh.B && long_batch(sh, max_total)) p->cols = 0;
+  if (p->cols == 16 && (long long)n_rows * hpr <= 8ll * sh.B && long_batch(sh, page, max_total)) p->cols = 0;
   if (!p->cols) {
     p->rows = tc ? PagedPlan::kTc : PagedPlan::kSimt;
     if (!tc && !gva::paged_simt_supported(sh))
