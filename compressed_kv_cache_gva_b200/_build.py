@@ -14,6 +14,7 @@ import hashlib
 import os
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -84,12 +85,22 @@ def build_bind(force: bool = False) -> str:
     return BIND
 
 
+def _try_bind(force: bool = False) -> None:
+    """The C library needs nvcc only: without torch, its headers or a host compiler it is
+    built all the same, and the paged calls of the Python binding then say what is missing."""
+    try:
+        build_bind(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn(f"libgva.so is built, the Python binding of its paged calls is not: {e}")
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
     """Compile every csrc/*.cu and link them into `out` (default: the package's
-    libgva.so).  `extra_flags` go to every nvcc compile (e.g. -DGVA_TRACE)."""
+    libgva.so), then the Python binding where it can be built.  `extra_flags` go to every
+    nvcc compile (e.g. -DGVA_TRACE)."""
     if not force and up_to_date(out) and (not extra_flags or out != LIB):
         if out == LIB:
-            build_bind()
+            _try_bind()
         return out
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = _sources()
@@ -115,7 +126,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str =
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, out)
     if out == LIB:
-        build_bind(force)
+        _try_bind(force)
     return out
 
 
