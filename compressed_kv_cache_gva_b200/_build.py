@@ -14,6 +14,7 @@ import hashlib
 import os
 import subprocess
 import sys
+import sysconfig
 import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -56,24 +57,25 @@ def up_to_date(out: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-# Python binding of the paged serving calls: reads torch tensors directly.
-BIND = os.path.join(PKG, "_bind.so")
+def bind_path() -> str:
+    """The Python binding of the paged serving calls.  It reads torch tensors directly, so it
+    fits the interpreter and the torch that it was compiled against and carries their names."""
+    import torch
+    return os.path.join(PKG, f"_bind.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
 
 
 def build_bind(force: bool = False) -> str:
     """Compile csrc/bind.cpp against torch's headers and libgva.so."""
-    src = os.path.join(CSRC, "bind.cpp")
+    src, out = os.path.join(CSRC, "bind.cpp"), bind_path()
     deps = [src, os.path.abspath(__file__), *glob.glob(os.path.join(INCLUDE, "*.h"))]
-    if not force and os.path.exists(BIND) and all(os.path.getmtime(p) <= os.path.getmtime(BIND) for p in deps):
-        return BIND
-    import sysconfig
-
+    if not force and os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
+        return out
     import torch
     from torch.utils.cpp_extension import include_paths
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     incs = [*include_paths(), os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
             sysconfig.get_path("include")]
-    tmp = BIND + ".tmp"
+    tmp = out + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *[a for i in incs for a in ("-isystem", i)], src, "-o", tmp, "-L" + PKG, "-l:" + os.path.basename(LIB),
@@ -81,8 +83,8 @@ def build_bind(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"building the Python binding failed:\n{r.stderr}")
-    os.replace(tmp, BIND)
-    return BIND
+    os.replace(tmp, out)
+    return out
 
 
 def _try_bind(force: bool = False) -> None:

@@ -283,7 +283,8 @@ def _paged():
     global _bind
     if _bind is None:
         lib()
-        path = os.path.join(_PKG, "_bind.so")
+        from ._build import bind_path
+        path = bind_path()
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with "
                                "`python -m compressed_kv_cache_gva_b200._build`")
