@@ -43,11 +43,12 @@ def _deps():
 # after 50 ms, and the split kernel's producer never requests the second tile of
 # each CTA, so a consumer wait runs out (no copy is ever in flight for that tile).
 # LANE_EXPIRY set in a paged call's status word makes waits run out in half of each
-# warp's lanes as well.
+# warp's lanes as well; GVA_TEST_CLUSTER_LIMIT in the environment bounds the page plan's
+# cluster, as a partition of the GPU would.
 WAIT_TEST_LIB = os.path.join(PKG, "libgva_waittest.so")
 LANE_EXPIRY = 1 << 30
 WAIT_TEST_FLAGS = ("-DGVA_WAIT_NS=50000000ull", "-DGVA_TEST_WITHHOLD_TILE=1",
-                   f"-DGVA_TEST_LANE_EXPIRY={LANE_EXPIRY}")
+                   f"-DGVA_TEST_LANE_EXPIRY={LANE_EXPIRY}", "-DGVA_TEST_CLUSTER_LIMIT")
 
 
 def up_to_date(out: str = LIB) -> bool:

@@ -31,6 +31,12 @@ cudaError_t ensure_max_smem(void (*k)(KArgs...), size_t smem) {
   return e;
 }
 
+// The largest cluster of `want`, want / 2, ... 1 blocks that the current context can hold:
+// a partition of the GPU may have no cluster's worth of SMs side by side.  The kernel's
+// attributes for `smem` and for more than 8 blocks are set.  Asked once per kernel, context
+// and block size.
+int cluster_that_fits(const void* kernel, int want, int threads, size_t smem);
+
 // Launch with programmatic stream serialization allowed (see pdl_wait).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,

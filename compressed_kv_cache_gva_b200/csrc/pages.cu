@@ -263,9 +263,11 @@ cudaError_t launch_plan_pages(const PlanArgs& a, cudaStream_t st) {
   if (threads * kPlanPer < a.B) threads = kPlanMaxThreads;
   // One CTA for small steps; else a cluster of 16 (the most there is, opt-in): the step
   // of 2048 requests and 39102 new tokens takes 13.4 us with 16 CTAs, 15.8 with 8.
-  const int cl = (a.B > 512 || a.max_new > 4096) ? kPlanCluster : 1;
-  const size_t smem = sizeof(int) * (size_t)(6 * a.B + 3);
-  cudaError_t e = ensure_max_smem(plan_pages_kernel, smem);
+  // (Any size works; a context that cannot hold 16 takes the largest half, quarter, ... of
+  // it that fits.)
+  int cl = (a.B > 512 || a.max_new > 4096) ? kPlanCluster : 1;
+  const size_t smem = sizeof(int) * (size_t)(6 * a.B + 3), most = sizeof(int) * (size_t)(6 * kMaxBatch + 3);
+  cudaError_t e = ensure_max_smem(plan_pages_kernel, most);
   if (e != cudaSuccess) return e;
   const void* key = reinterpret_cast<const void*>(plan_pages_kernel);
   const int wide = (int)cudaFuncAttributeNonPortableClusterSizeAllowed;
@@ -274,6 +276,7 @@ cudaError_t launch_plan_pages(const PlanArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr_record(key, wide, 1);
   }
+  if (cl > 1) cl = cluster_that_fits(key, cl, threads, most);
   return launch_pdl_cluster(plan_pages_kernel, dim3(cl), dim3(threads), cl, smem, st, a, cl);
 }
 

@@ -462,7 +462,7 @@ gva_status_t gva_noalloc_status(int32_t* status_out, void* stream);
  *   err_flag      device int32 or NULL: GVA_DEVERR_* bits are or-ed in, never cleared
  * One launch.  Inputs and outputs other than the pairs named above must not overlap.
  * The entries of held_in and free_count_in are all read before any output is written.
- * Errors: GVA_ERR_INVALID_ARG.  B == 0 sets q_start[0] = 0, the slots to -1 and the
+ * Errors: GVA_ERR_INVALID_ARG; GVA_ERR_CUDA where a launch fails.  B == 0 sets q_start[0] = 0, the slots to -1 and the
  * count.
  */
 gva_status_t gva_plan_pages(int32_t B, int32_t page_size, int32_t num_pages, int32_t max_pages,
@@ -572,7 +572,8 @@ gva_status_t gva_paged_attention(const gva_shape_t* shape, int32_t page_size, co
  *   err_flag   device int32 or NULL: GVA_DEVERR_RANGE is or-ed in by a draft outside
  *              [0, vocab) (it counts as refused), a row without any probability (it
  *              gives vocab - 1) or a row range outside [0, n_rows) (skipped)
- * One launch, no workspace.  Errors: GVA_ERR_INVALID_ARG.  B == 0 is a no-op.
+ * One launch, no workspace.  Errors: GVA_ERR_INVALID_ARG; GVA_ERR_CUDA where a launch
+ * fails.  B == 0 is a no-op.
  */
 gva_status_t gva_verify_draft(int32_t B, int32_t vocab, int32_t n_rows, const int32_t* tokens,
                               const int32_t* q_start, int32_t probs_dtype,
