@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
     for (int u = 0; u < PPT; ++u) {
       if (c0 + u * npg >= n) break;
-      if (e[u].x == -INFINITY) continue;          // piece past this query's causal limit
+      if (e[u].y == 0.f) continue;                // piece past this query's causal limit
       const float mn = fmaxf(m, e[u].x);
       const float f = ex2(m - mn), w = ex2(e[u].x - mn);
       l = l * f + w * e[u].y;
@@ -131,19 +131,18 @@ __global__ void __launch_bounds__(1024)
   for (int u = 0; u < npg; ++u) M = fmaxf(M, sm_m[u][lane]);
   float L = 0.f, O = 0.f;
   for (int u = 0; u < npg; ++u) {
-    const float mu = sm_m[u][lane];
-    if (mu == -INFINITY) continue;                 // a group that saw no piece
-    const float f = ex2(mu - M);
+    if (sm_l[u][lane] == 0.f) continue;            // a group that saw no piece
+    const float f = ex2(sm_m[u][lane] - M);
     L = fmaf(f, sm_l[u][lane], L);
     O = fmaf(f, sm_o[u][lane], O);
   }
   if (col) {
-    const float v = L > 0.f ? O / L : 0.f;
+    const float v = L == 0.f ? 0.f : O / L;
     if constexpr (sizeof(TO) == 2) out[((size_t)b * H + h) * d_h + d] = __float2bfloat16_rn(v);
     else out[((size_t)b * H + h) * d_h + d] = v;
   }
   if (lane == 0 && blockIdx.z == 0 && lse)
-    lse[(size_t)b * H + h] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    lse[(size_t)b * H + h] = natural_lse(M, L);
 #ifdef GVA_TRACE
   if (a.trace && tid == 0 && cid < 16384) {
     unsigned long long tt;
@@ -194,23 +193,28 @@ __global__ void __launch_bounds__(128)
   pdl_trigger();   // as in the combine: successors wait before they read
   pdl_wait();
   float mx = -INFINITY;
-  for (int r = 0; r < R; ++r) mx = fmaxf(mx, lses[(size_t)r * BH + bh]);
+  bool seen = false;                               // some part's lse is a number or NaN
+  for (int r = 0; r < R; ++r) {
+    const float l = lses[(size_t)r * BH + bh];
+    seen |= l != -INFINITY;
+    mx = fmaxf(mx, l);
+  }
   float z = 0.f;
-  if (mx != -INFINITY)
+  if (seen)
     for (int r = 0; r < R; ++r) z += ex2((lses[(size_t)r * BH + bh] - mx) * kLog2e);
   for (int d = threadIdx.x; d < d_h; d += blockDim.x) {
     float acc = 0.f;
-    if (mx != -INFINITY)
+    if (seen)
       for (int r = 0; r < R; ++r) {
         const float l = lses[(size_t)r * BH + bh];
         if (l == -INFINITY) continue;              // an empty part contributes nothing
         acc = fmaf(ex2((l - mx) * kLog2e), outs[((size_t)r * BH + bh) * d_h + d], acc);
       }
-    const float v = mx != -INFINITY ? acc / z : 0.f;
+    const float v = seen ? acc / z : 0.f;
     if constexpr (sizeof(TO) == 2) out[(size_t)bh * d_h + d] = __float2bfloat16_rn(v);
     else out[(size_t)bh * d_h + d] = v;
   }
-  if (threadIdx.x == 0 && lse) lse[bh] = mx != -INFINITY ? mx + log2f(z) * kLn2 : -INFINITY;
+  if (threadIdx.x == 0 && lse) lse[bh] = seen ? mx + log2f(z) * kLn2 : -INFINITY;
 }
 
 cudaError_t launch_merge_states(const gva_shape_t& sh, int R, const float* outs, const float* lses,

@@ -73,6 +73,15 @@ __host__ __device__ inline WsLayout ws_layout(int B, int H, int d_h, int grid, i
   return w;
 }
 
+// A row's softmax state is (m, l): the reference its exponentials are taken against and
+// their sum.  l = 0 exactly where the row saw no key (the largest exponential is at least
+// 1 otherwise); a NaN score leaves l NaN, and m -inf where every score is NaN, since a
+// maximum passes NaN over.  So l alone tells "no key" (0 and -inf) from NaN.
+__device__ __forceinline__ float norm_of(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float natural_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
 struct DecodeArgs {
   int B, H, G, d_h, d_r;
   const float* q_abs;        // GVA: [B,H,d_h+d_r] float32, pre-scaled to base-2 units

@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         p[h] = (live && m_ref[h] != -INFINITY) ? ex2(s[h] - m_ref[h]) : 0.f;
-        l[h] += p[h];
+        l[h] += live && s[h] != s[h] ? s[h] : p[h];   // a NaN score shows in the sum
       }
       // P buffer k % NPB is free once the P.V of tile k - NPB has completed
       if (k >= C::NPB) {

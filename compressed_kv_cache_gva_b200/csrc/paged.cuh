@@ -20,15 +20,6 @@ __device__ __forceinline__ void pdl_leave(const PagedArgs& a) {
   if (a.beside) pdl_wait();
 }
 
-// A row's softmax state is (m, l): the reference its exponentials are taken against and
-// their sum.  l = 0 exactly where the row saw no key (the largest exponential is at least
-// 1 otherwise); a NaN score leaves l NaN, and m -inf where every score is NaN, since a
-// maximum passes NaN over.  So l alone tells "no key" (0 and -inf) from NaN.
-__device__ __forceinline__ float norm_of(float l) { return l == 0.f ? 0.f : 1.f / l; }
-__device__ __forceinline__ float natural_lse(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
 // Query rows [r0, r0 + n) and cached length of sequence b; n = 0 where the sequence
 // is inconsistent or belongs to the other kernel of the call.
 struct SeqRows {

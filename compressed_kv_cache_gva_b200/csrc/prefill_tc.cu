@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     // ---- output: O / l (zero and lse = -inf for a query that sees no cache row)
     const size_t orow = ((size_t)b * nq + qi) * a.H + head;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = norm_of(l);
 #pragma unroll
     for (int q4 = 0; q4 < C::D_H / 16; ++q4) {
       float o[16];
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
     }
-    if (valid && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (valid && a.lse) a.lse[orow] = natural_lse(m, l);
     (void)ok;
   }
 

@@ -177,7 +177,8 @@ size_t gva_decode_workspace_size(const gva_shape_t* shape, int64_t max_total_tok
  *   max_total_tokens  upper bound of sum(seq_len) (host value, sizes the split)
  *   out        device [B, H, d_h] out_dtype   o_h = sum_j p_j v_{j,g(h)}
  *   lse        device [B, H] float32 or NULL: natural-log log-sum-exp of the scaled
- *              scores (-inf for an empty sequence, whose output is 0)
+ *              scores (-inf for an empty sequence, whose output is 0); a query that holds
+ *              a NaN makes its own row of out and lse NaN and no other
  *   workspace  device, ws_bytes >= gva_decode_workspace_size(shape, max_total_tokens)
  * Alignment: 16 bytes for all pointers; V_cache rows (G*d_h*elt) and k_rope rows
  * (d_r*elt) must be multiples of 16 bytes.  Concurrent calls on different streams
