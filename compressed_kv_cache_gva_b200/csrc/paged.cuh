@@ -107,27 +107,36 @@ __device__ __forceinline__ int slot_of(const PagedArgs& a, const int* row, int t
 // [i, i+1) * NT / grid; a block whose tiles fall to several CTAs is merged from their
 // pieces.
 // ---------------------------------------------------------------------------
-// Sum over i in [0, n) of floor((a i + b) / m), all >= 0 (the Euclidean recursion on
-// the lattice points under a line).
+// Terms floor(j / h) over j < x: q = floor(x / h) whole steps of h equal terms 0 .. q-1, and
+// the rest at height q.
 template <typename U>
-__device__ inline unsigned long long floor_sum(U n, U m, U a, U b) {
-  unsigned long long sum = 0;
-  for (;;) {
-    if (a >= m) {
-      sum += (unsigned long long)n * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      sum += (unsigned long long)n * (b / m);
-      b %= m;
-    }
-    const U y = a * n + b;   // within U where the first a n + b is
-    if (y < m) return sum;
-    n = y / m;
-    b = y % m;
-    const U t = m;
-    m = a;
-    a = t;
+__device__ __forceinline__ unsigned long long steps_below(U x, U h) {
+  const U q = x / h;
+  const unsigned long long w = q;
+  return h * (w * (w - (w > 0)) / 2) + w * (x - q * h);
+}
+// The same over every second j from c on, n of them.  Added up with its neighbour j + 1 each
+// term counts twice, except where j + 1 is a multiple of h and the neighbour is one higher.
+// For even h the pair (2i, 2i + 1) shares one term.  For odd h the multiples in question are
+// those of c + 1's parity, every second one: y0 mod 2h.
+template <typename U>
+__device__ inline unsigned long long alternate_steps(U c, U n, U h) {
+  if (h % 2 == 0) return steps_below<U>(c / 2 + n, h / 2) - steps_below<U>(c / 2, h / 2);
+  const U last = c + 2 * n, y0 = c % 2 ? 0 : h, p = 2 * h;
+  const U higher = (last + p - y0) / p - (c + p - y0) / p;
+  return (steps_below<U>(last, h) - steps_below<U>(c, h) - higher) / 2;
+}
+// Sum over i in [0, n) of floor((M i + b) / (h TK)): M and TK are powers of two, so the quotient
+// by the smaller one is exact and leaves a staircase of steps h TK / M, or h at every second place.
+// Out of line: inlined in every prologue it cost a step of drafts 30.2 -> 30.9 us.
+template <int M, int TK, typename U>
+__device__ __noinline__ unsigned long long line_floors(U n, U h, unsigned long long b) {
+  static_assert(TK % M == 0 || M == 2 * TK, "tiles of these kernels");
+  if constexpr (TK % M == 0) {
+    const U c = (U)(b / M), p = h * (TK / M);
+    return steps_below<U>(c + n, p) - steps_below<U>(c, p);
+  } else {
+    return alternate_steps<U>((U)(b / TK), n, h);
   }
 }
 
@@ -154,9 +163,9 @@ struct RowBlocks {
       // full blocks: ceil((L - n + floor(((rb + 1) M - 1) / hpr) + 1) / TK), one floor
       // of a line in rb
       const unsigned long long h = a.hpr, b = M - 1 + h * (unsigned long long)(s.L - s.n + TK);
-      u += b + (unsigned long long)M * nb < (1ull << 32) && h * TK < (1ull << 32)
-               ? (long long)floor_sum<unsigned>(nb - 1, (unsigned)(h * TK), M, (unsigned)b)
-               : (long long)floor_sum<unsigned long long>(nb - 1, h * TK, M, b);
+      u += b + (unsigned long long)M * nb < (1ull << 31) && h * TK < (1ull << 31)
+               ? (long long)line_floors<M, TK, unsigned>(nb - 1, (unsigned)h, b)
+               : (long long)line_floors<M, TK, unsigned long long>(nb - 1, h, b);
     }
     return (u + (long long)OV * nb) * a.G;
   }

@@ -36,6 +36,19 @@ def test_row_blocks_of_many_requests(case, out):
     x.check(x.run(out, ctas=1), ref, out, 2.0 ** -8 if out == BF else 2.0 ** -16)
 
 
+# more than four blocks of a request, whose tiles are counted in closed form: heads per group
+# odd and even, tiles of 64 keys (float32 output of d_h = 64) and of 128
+CHUNKS = [(A, 16, [500, 41], [200, 41]), ((12, 4, 64, 8), 16, [600, 300], [300, 201]), ((10, 2, 64, 0), 32, [450], [333]),
+          ((6, 2, 128, 16), 64, [700, 400], [300, 260]), ((8, 1, 128, 16), 16, [333], [150]), ((7, 1, 64, 8), 16, [333], [151])]
+
+
+@pytest.mark.parametrize("case", range(len(CHUNKS)))
+@pytest.mark.parametrize("out", [F32, BF])
+def test_chunks_of_many_blocks(case, out):
+    x = Batch(*CHUNKS[case], pad=case % 2, seed=case)
+    x.check(x.run(out), x.reference(), out, 2.0 ** -8 if out == BF else 2.0 ** -16)
+
+
 @pytest.mark.parametrize("heads,new", [((4, 1, 64, 16), [3, 4, 2, 0]), ((8, 2, 64, 16), [1] * 7 + [9])])
 def test_the_largest_batch(heads, new):
     B = 4096

@@ -44,3 +44,37 @@ def test_every_tile_once_and_every_piece_merged(M, TK, OV, seed):
             merged.add(s)
         assert at == nt
     assert merged == set(slots)
+
+
+def steps_below(x, h):
+    q = x // h
+    return h * (q * (q - 1) // 2) + q * (x - q * h)
+
+
+def line_floors(M, TK, n, h, b):
+    """Sum over i < n of (M i + b) // (h TK), in the kernels' closed form."""
+    if TK % M == 0:
+        c, p = b // M, h * (TK // M)
+        return steps_below(c + n, p) - steps_below(c, p)
+    c = b // TK
+    if h % 2 == 0:
+        return steps_below(c // 2 + n, h // 2) - steps_below(c // 2, h // 2)
+    last, y0, p = c + 2 * n, 0 if c % 2 else h, 2 * h
+    higher = (last + p - y0) // p - (c + p - y0) // p
+    total = steps_below(last, h) - steps_below(c, h) - higher
+    assert total % 2 == 0
+    return total // 2
+
+
+@pytest.mark.parametrize("M,TK", [(128, 64), (128, 128), (16, 32)])
+@pytest.mark.parametrize("h", [1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 33, 64])
+def test_tiles_of_a_sequence_without_a_loop(M, TK, h):
+    rng = np.random.default_rng(h)
+    for _ in range(150):
+        n = int(rng.integers(1, 3000))
+        L = n + int(rng.integers(0, 20000))
+        nb = -(-n * h // M)
+        got = line_floors(M, TK, nb - 1, h, M - 1 + h * (L - n + TK))
+        assert got == sum(tiles(n, L, h, rb, M, TK) for rb in range(nb - 1))
+        b, k = int(rng.integers(0, 10 ** 6)), int(rng.integers(0, 200))
+        assert line_floors(M, TK, k, h, b) == sum((M * i + b) // (h * TK) for i in range(k))
