@@ -34,10 +34,13 @@ constexpr int kPlanPer = kMaxBatch / kPlanMaxThreads;   // requests per thread a
 constexpr int kPlanCluster = 16;                        // CTAs of a large step
 constexpr int kTok = 4;                                 // new tokens per thread in flight
 
+// (Both want whole warps together: the loops before them let lanes leave early.)
 __device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

@@ -39,10 +39,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// (Both want whole warps together.)
 __device__ __forceinline__ void cl_arrive() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cl_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // A double from the same shared-memory offset of another CTA of the cluster.
@@ -399,7 +402,6 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs 
     }
   }
   __threadfence();   // no early trigger: the next step's calls read these lengths
-  __syncwarp();
   if (cl > 1) cl_wait();
 }
 
