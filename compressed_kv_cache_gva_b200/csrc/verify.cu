@@ -13,12 +13,13 @@
 //
 // What bounds it: memory.  Besides k probabilities a request reads one row of each
 // model, vocab * 2 * 4 bytes, once.  A cluster of CTAs shares a request: each warp
-// sums a contiguous chunk through a ring in shared memory, four CTAs per SM, the
-// chunk sums meet through distributed shared memory, and the CTA whose chunk
+// sums a contiguous chunk through a ring in shared memory, up to three CTAs per SM,
+// the chunk sums meet through distributed shared memory, and the CTA whose chunk
 // holds the answer reads it again from L2, an eighth per warp.
-// Sums are in 64 bits: with ~10^5 tokens of mass ~10^-5 each, 32-bit running sums
-// are off by a good part of a token's mass, and the drawn token would depend on the
-// order of the additions.
+// Sums keep 48 bits (64-bit sums of pairs, whose exact rounding errors are summed in
+// 32; see chunk_sum_of): with ~10^5 tokens of mass ~10^-5 each, 32-bit running sums are
+// off by a good part of a token's mass, and the drawn token would depend on the order
+// of the additions.
 #include "common.cuh"
 #include "launch.h"
 #include "paged.h"

@@ -555,7 +555,7 @@ gva_status_t gva_paged_attention(const gva_shape_t* shape, int32_t page_size, co
  * after a refusal (target without x if draft_probs is NULL; target itself if that
  * leaves nothing), w = target of row k when all are accepted; it is the first v with
  *     w_0 + ... + w_v > u_sample[b] * sum(w),
- * sums in 64 bits.  Weights that are not > 0, NaN included, count as 0; weights are
+ * sums to 2^-48 of themselves.  Weights that are not > 0, NaN included, count as 0; weights are
  * otherwise finite.
  *
  *   vocab      in [1, 2^30];  n_rows: rows of the buffers, at most 2^31 - 1025;  B in [0, 65535]
