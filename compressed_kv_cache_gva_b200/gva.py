@@ -314,6 +314,8 @@ def plan_pages(page_size: int, num_pages: int, kept_len, n_new, held_in, held_ou
 
 def paged_workspace_size(shape: Shape, page_size: int, n_rows: int, max_query_len: int,
                          max_total_tokens: int) -> int:
+    """Bytes that serve every paged_attention call of these heads, types and page size with no
+    more requests, rows, new tokens per request or cached tokens."""
     return int(lib().gva_paged_workspace_size(ctypes.byref(shape), int(page_size), int(n_rows),
                                               int(max_query_len), int(max_total_tokens)))
 
@@ -347,7 +349,7 @@ def verify_draft(vocab: int, tokens, q_start, target_probs, draft_probs, u_accep
     tokens, out_tokens [n_rows] int32; q_start [B + 1] int32; target_probs and draft_probs
     [n_rows, >= vocab] float32 or bfloat16 (rows may be strided; draft_probs None: the
     drafts were not drawn); u_accept [n_rows], u_sample [B] float32; n_accepted, seq_len,
-    kept_len [B] int32."""
+    kept_len [B] int32.  out_tokens must not overlap tokens; kept_len may be seq_len."""
     _check((_bind or _paged()).verify_draft(
         vocab, tokens, q_start, target_probs, draft_probs, u_accept, u_sample, out_tokens, n_accepted,
         seq_len, kept_len, err_flag, _handle(stream)))

@@ -99,3 +99,14 @@ def test_two_warps_per_group_keep_p_in_two_parts(case):
     """The bf16 output of 9 to 16 columns, to the bound of probabilities in two bf16 parts."""
     x = Batch(*SIXTEEN[case], pad=case % 3, seed=case, stride=case % 2)
     x.check(x.run(BF), x.reference(), BF, 2.0 ** -16)
+
+
+@pytest.mark.parametrize("new,out", [([1, 1, 2], F32), ([20, 20, 1], BF)])
+def test_requests_that_share_pages(new, out):
+    """A common prefix: two requests name the same pages, a third the first of them."""
+    x = Batch(A, 16, [100, 100, 64], new, seed=2)
+    x.table[1] = x.table[0]
+    x.table[2, :4] = x.table[0, :4]
+    x.q[new[0]:2 * new[0]] = x.q[:new[0]]
+    got = x.run(out)
+    x.check(got, x.reference(), out, 2.0 ** -8 if out == BF else 2.0 ** -16)
